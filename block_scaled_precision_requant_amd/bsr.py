@@ -32,6 +32,14 @@ SIGNATURES = {
     "int8_gemm_blockscaled_ws_bytes": (ctypes.c_uint64, [_u32, _u32, _u32]),
     "int8_gemm_blockscaled_ws": (_int, [_vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _vp, ctypes.c_uint64, _vp]),
     "int8_gemm_blockscaled_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _vp]),
+    "moe_route_ws_bytes": (ctypes.c_uint64, [_u32, _u32, _u32]),
+    "moe_route": (_int, [_vp, _int, _u32, _vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _int, _int, _f32, _vp,
+                         ctypes.c_uint64, _vp]),
+    "int8_grouped_gemm_blockscaled": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _u32, _u32, _vp]),
+    "moe_combine": (_int, [_vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _u32, _vp]),
+    "w4a16_group_gemv": (_int, [_vp, _vp, _vp, _int, _vp, _u32, _vp, _u32, _u32, _u32, _vp]),
+    "w4a16_group_gemv_experts": (_int, [_vp, _vp, _vp, _int, _vp, _u32, _vp, _vp, _int, _vp, _u32, _u32, _u32, _u32,
+                                        _u32, _vp]),
     "bsr_status_string": (ctypes.c_char_p, [_int]),
 }
 
@@ -82,7 +90,7 @@ def _stream(stream, like):
 # Element kinds the kernels read and write: byte codes (int8, packed E2M1,
 # E4M3), 16-bit BF16 bits (any 2-byte dtype: torch.bfloat16, int16, uint16)
 # and binary32 scales.
-BYTES, BF16, F32 = "1-byte", "2-byte", "float32"
+BYTES, BF16, F32, I32 = "1-byte", "2-byte", "float32", "int32"
 
 
 def _shape(t, shape, what, kind):
@@ -94,7 +102,7 @@ def _shape(t, shape, what, kind):
 
 
 def _kind(t, what, kind):
-    ok = (t.dtype == torch.float32 if kind == F32 else
+    ok = (t.dtype == (torch.float32 if kind == F32 else torch.int32) if kind in (F32, I32) else
           t.element_size() == (1 if kind == BYTES else 2) and not t.dtype.is_complex)
     if not ok:
         raise ValueError(f"{what}: dtype {t.dtype}, expected {kind} elements")
@@ -268,3 +276,146 @@ def prefill(a_bf16, w_i8, w_scale, a_i8_scratch, a_scale_scratch, out, stream=No
     """The two-launch projection: requant_a_int8 then int8_gemm_blockscaled on one stream."""
     requant_a_int8(a_bf16, a_i8_scratch, a_scale_scratch, stream=stream)
     int8_gemm_blockscaled(a_i8_scratch, w_i8, a_scale_scratch, w_scale, out, stream=stream)
+
+
+# ---- expert layers and integer 4-bit weights --------------------------------
+
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2
+
+
+def _type(t, what):
+    """Element type of an argument that takes three: float32, float16, or BF16 (any
+    other 2-byte dtype, as raw bits)."""
+    if t.dtype == torch.float32:
+        return TYPE_F32
+    if t.dtype == torch.float16:
+        return TYPE_F16
+    _kind(t, what, BF16)
+    return TYPE_BF16
+
+
+def _launch(name, stream, tensors, args):
+    """Calls an entry point with the tensors' device as the current one, on `stream`
+    (default: torch's current stream there)."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"arguments on {dev} and {t.device}: all must be on one device")
+    if dev.type != "cuda":
+        raise ValueError("arguments must be device tensors")
+    with torch.cuda.device(dev):
+        _done(getattr(lib(), name)(*args, _stream(stream, tensors[0])), name)
+
+
+def moe_route_ws_bytes(tokens, experts, top_k):
+    """Workspace bytes moe_route needs; 0 for few tokens, at most 1024 * experts."""
+    return int(lib().moe_route_ws_bytes(int(tokens), int(experts), int(top_k)))
+
+
+def moe_route(logits, ids, weights, offsets, row_token, pos, workspace=None, score=SCORE_SOFTMAX, renorm=True,
+              scale=1.0, stream=None):
+    """Router: logits [T,E] (BF16, float16 or float32; rows may be strided) -> ids [T,k] int32, weights [T,k]
+    float32, and the routed rows in expert order: offsets [E+1], row_token [T*k], pos [T,k] (all int32).
+    workspace: a device tensor of at least moe_route_ws_bytes(T, E, k) bytes, or None when that is 0."""
+    t, e = logits.shape
+    if ids.dim() != 2:
+        raise ValueError(f"ids: shape {tuple(ids.shape)}, expected two dimensions")
+    k = ids.shape[1]
+    kind = _type(logits, "logits")
+    if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
+        raise ValueError("logits: rows with unit column stride that do not overlap")
+    for x, shape, what, dt in ((ids, (t, k), "ids", I32), (weights, (t, k), "weights", F32),
+                               (offsets, (e + 1,), "offsets", I32), (row_token, (t * k,), "row_token", I32),
+                               (pos, (t, k), "pos", I32)):
+        _shape(x, shape, what, dt)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _launch("moe_route", stream, (offsets, logits, ids, weights, row_token, pos, workspace),
+            (_ptr(logits), kind, logits.stride(0) if t > 1 else e, _ptr(ids), _ptr(weights), _ptr(offsets),
+             _ptr(row_token), _ptr(pos), t, e, k, int(score), int(bool(renorm)), float(scale), _ptr(workspace),
+             ws_bytes))
+
+
+def _grouped_shapes(offsets, row_index, out, cols, experts):
+    rows = out.shape[0]
+    _shape(out, (rows, cols), "out", BF16)
+    _shape(offsets, (experts + 1,), "offsets", I32)
+    if row_index is not None:
+        _shape(row_index, (rows,), "row_index", I32)
+    return rows
+
+
+def int8_grouped_gemm_blockscaled(a_i8, w_i8, a_scale, w_scale, offsets, out, row_index=None, stream=None):
+    """Products grouped by expert: out[p] (BF16, rows offsets[e]..offsets[e+1]-1) = row row_index[p] (p without it)
+    of a_i8 [A,K] / a_scale [A,K/32] times the weight w_i8 [E,N,K] / w_scale [E,N,K/32] of expert e."""
+    a_rows, k = a_i8.shape
+    e, n, _ = w_i8.shape
+    _shape(a_i8, (a_rows, k), "a_i8", BYTES)
+    _shape(w_i8, (e, n, k), "w_i8", BYTES)
+    _shape(a_scale, (a_rows, k // 32), "a_scale", F32)
+    _shape(w_scale, (e, n, k // 32), "w_scale", F32)
+    rows = _grouped_shapes(offsets, row_index, out, n, e)
+    _launch("int8_grouped_gemm_blockscaled", stream, (out, a_i8, w_i8, a_scale, w_scale, offsets, row_index),
+            (_ptr(a_i8), _ptr(w_i8), _ptr(a_scale), _ptr(w_scale), _ptr(offsets), _ptr(row_index), _ptr(out), a_rows,
+             rows, e, n, k))
+
+
+def moe_combine(y, pos, weights, out, residual=None, stream=None):
+    """out [T,N] BF16 = residual + sum over the slots s of weights[t,s] * y[pos[t,s]] (y [R,N] BF16; a pos outside
+    0..R-1 adds nothing)."""
+    rows, n = y.shape
+    t, k = pos.shape
+    _shape(y, (rows, n), "y", BF16)
+    _shape(pos, (t, k), "pos", I32)
+    _shape(weights, (t, k), "weights", F32)
+    _shape(out, (t, n), "out", BF16)
+    if residual is not None:
+        _shape(residual, (t, n), "residual", BF16)
+    _launch("moe_combine", stream, (out, y, pos, weights, residual),
+            (_ptr(y), _ptr(pos), _ptr(weights), _ptr(residual), _ptr(out), t, k, rows, n))
+
+
+def _w4_shapes(x, w_packed, scale, zero):
+    """(lead, n, k, group, scale type) of a 4-bit weight w_packed [*lead, N, K/2] for x [M, K]."""
+    k = x.shape[1]
+    lead, n = tuple(w_packed.shape[:-2]), w_packed.shape[-2]
+    _shape(x, tuple(x.shape[:1]) + (k,), "x_bf16", BF16)
+    _shape(w_packed, lead + (n, k // 2), "w_packed", BYTES)
+    cols = scale.shape[-1]
+    if cols == 0 or k % cols:
+        raise ValueError(f"scale: {cols} groups do not divide K = {k}")
+    kind = _type(scale, "scale")
+    if tuple(scale.shape) != lead + (n, cols) or not scale.is_contiguous():
+        raise ValueError(f"scale: shape {tuple(scale.shape)}, expected contiguous {lead + (n, cols)}")
+    if zero is not None:
+        _shape(zero, lead + (n, cols), "zero", BYTES)
+    return lead, n, k, 0 if cols == 1 else k // cols, kind
+
+
+def w4a16_group_gemv(x_bf16, w_packed, scale, out, zero=None, stream=None):
+    """out [M,N] BF16 = x_bf16 [M,K] times the 4-bit weight scale * (code - zero): w_packed [N,K/2] (low nibble
+    first), scale [N,K/group] (BF16, float16 or float32; one column: one scale per row), zero [N,K/group] uint8 or
+    None (8 throughout)."""
+    lead, n, k, group, kind = _w4_shapes(x_bf16, w_packed, scale, zero)
+    if lead:
+        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected two dimensions")
+    m = x_bf16.shape[0]
+    _shape(out, (m, n), "out", BF16)
+    _launch("w4a16_group_gemv", stream, (out, x_bf16, w_packed, scale, zero),
+            (_ptr(x_bf16), _ptr(w_packed), _ptr(scale), kind, _ptr(zero), group, _ptr(out), m, n, k))
+
+
+def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, row_index=None, silu_mul=False,
+                             stream=None):
+    """w4a16_group_gemv by expert (w_packed [E,N,K/2], scale and zero [E,N,K/group]); offsets and row_index as
+    int8_grouped_gemm_blockscaled.  silu_mul: the first N/2 columns are gates, the others ups, and out [R,N/2] is
+    SiLU(gate) * up."""
+    lead, n, k, group, kind = _w4_shapes(x_bf16, w_packed, scale, zero)
+    if len(lead) != 1:
+        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected three dimensions")
+    rows = _grouped_shapes(offsets, row_index, out, n // 2 if silu_mul else n, lead[0])
+    _launch("w4a16_group_gemv_experts", stream, (out, x_bf16, w_packed, scale, zero, offsets, row_index),
+            (_ptr(x_bf16), _ptr(w_packed), _ptr(scale), kind, _ptr(zero), group, _ptr(offsets), _ptr(row_index),
+             int(bool(silu_mul)), _ptr(out), x_bf16.shape[0], rows, lead[0], n, k))

@@ -1,10 +1,12 @@
 // api.hip -- the C ABI of libbsr: argument validation, the GEMV/GEMM dispatch
 // and the launches.  Every check happens before the first launch; an error
 // launches nothing.  The only state is a per-device cache of the gfx950 check.
+// The expert-layer entry points are in api_moe.hip.
 #include <atomic>
 #include <cmath>
 #include <cstring>
 
+#include "api_common.h"
 #include "bsr.h"
 #include "bsr_internal.h"
 
@@ -12,6 +14,10 @@ namespace {
 
 constexpr int kMaxDevices = 256;
 std::atomic<int> g_device_ok[kMaxDevices];  // 0 unknown, 1 gfx950, 2 other
+
+}  // namespace
+
+namespace bsr {
 
 int check_device() {
     int dev = -1;
@@ -27,7 +33,15 @@ int check_device() {
     return state == 1 ? BSR_OK : BSR_EDEVICE;
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace bsr
+
+using bsr::aligned;
+using bsr::check_device;
+using bsr::k_ok;
+using bsr::kMaxGrid;
+using bsr::launched;
+
+namespace {
 
 // Scratch of the allocation-free GEMM entry point: the K-split workspace of
 // int8_gemm_blockscaled_noalloc, one copy per GPU, held until the process
@@ -50,19 +64,12 @@ void *scratch_ptr() {
     return p;
 }
 
-bool k_ok(uint32_t k) { return k != 0 && k % 32 == 0; }
-
 // Rows the GEMV takes: one 16-row tile at any K, up to four when K suits the
 // streamed kernel.
 bool gemv_rows_ok(uint32_t m, uint32_t k) {
     return m <= (uint32_t)bsr::kGemvMaxRows ||
            (m <= (uint32_t)bsr::kGemvStreamMaxRows && k % bsr::kGemvStreamKAlign == 0);
 }
-
-// Grids stay below 2^31 workgroups.
-constexpr uint64_t kMaxGrid = (1ull << 31) - 1;
-
-int launched(hipError_t e) { return e == hipSuccess ? BSR_OK : BSR_ELAUNCH; }
 
 int gemm_args_check(const int8_t *a_i8, const int8_t *w_i8, const float *a_scale,
                     const float *w_scale, const uint16_t *out, uint32_t m, uint32_t n, uint32_t k,

@@ -1,0 +1,91 @@
+// moe_internal.h -- launchers and device helpers of the expert-layer kernels.
+#pragma once
+
+#include "bsr_internal.h"
+#include "moe_geometry.h"
+
+namespace bsr {
+
+// Launchers (no validation: the C-ABI layer has checked every argument).
+hipError_t launch_moe_route(const void *logits, int type, uint32_t ld, int32_t *ids, float *weights, int32_t *offsets,
+                            int32_t *row_token, int32_t *pos, uint32_t tokens, uint32_t experts, uint32_t top_k,
+                            bool sigmoid, bool renorm, float scale, uint32_t *hist, const RoutePlan &plan,
+                            hipStream_t s);
+hipError_t launch_moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, const uint16_t *residual,
+                              uint16_t *out, uint32_t tokens, uint32_t top_k, uint32_t rows, uint32_t n,
+                              hipStream_t s);
+
+// Rows of a grouped call: expert e owns rows [offsets[e], offsets[e + 1]) and
+// row p reads operand row index[p] (p where index is null).  offsets null: one
+// expert owns all rows.
+struct GroupedRows {
+    const int32_t *offsets;
+    const int32_t *index;
+    uint32_t src_rows, rows, experts;
+};
+
+hipError_t launch_grouped_gemm(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
+                               const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s);
+hipError_t launch_w4_group(const uint16_t *x, const uint8_t *w, const void *scale, int scale_type,
+                           const uint8_t *zero, uint32_t group, uint16_t *out, const GroupedRows &g, bool silu,
+                           uint32_t n, uint32_t k, hipStream_t s);
+
+#ifdef __HIPCC__
+struct RowTile {
+    uint32_t expert, row0, rows;  // rows == 0: no such tile
+};
+
+// Row tile v of tiles of bm rows.  Every lane of the wave must be active; the
+// result is the same in all of them.  offsets come from the device unchecked,
+// so each range is clamped to [0, rows].
+__device__ __forceinline__ RowTile find_row_tile(const GroupedRows &g, uint32_t bm, uint32_t v, int lane) {
+    if (g.offsets == nullptr) {
+        const uint32_t row0 = v * bm;
+        return {0, row0, row0 < g.rows ? min(bm, g.rows - row0) : 0};
+    }
+    uint32_t before = 0;  // tiles of the experts already passed
+    for (uint32_t e0 = 0; e0 < g.experts; e0 += 64) {
+        const uint32_t e = e0 + lane;
+        uint32_t lo = 0, hi = 0;
+        if (e < g.experts) {
+            lo = (uint32_t)min(max(g.offsets[e], 0), (int32_t)g.rows);
+            hi = (uint32_t)min(max(g.offsets[e + 1], (int32_t)lo), (int32_t)g.rows);
+        }
+        const uint32_t tiles = (hi - lo + bm - 1) / bm;
+        uint32_t incl = tiles;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = __shfl_up(incl, d);
+            if (lane >= d) incl += o;
+        }
+        const uint64_t past = __ballot(before + incl > v);
+        if (past != 0) {
+            const int owner = __builtin_ctzll(past);
+            const uint32_t first = before + __builtin_amdgcn_readlane(incl - tiles, owner);
+            const uint32_t olo = __builtin_amdgcn_readlane(lo, owner), ohi = __builtin_amdgcn_readlane(hi, owner);
+            const uint32_t row0 = olo + (v - first) * bm;
+            return {e0 + owner, row0, min(bm, ohi - row0)};
+        }
+        before += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return {0, 0, 0};
+}
+
+// Operand row of output row p, or -1 for a row of zeros.
+__device__ __forceinline__ int32_t source_row(const GroupedRows &g, uint32_t p) {
+    if (g.index == nullptr) return (int32_t)p;
+    const int32_t i = g.index[p];
+    return (uint32_t)i < g.src_rows ? i : -1;
+}
+
+// An element of `type` (enum bsr_type) as binary32 (exact).
+template <int TYPE>
+__device__ __forceinline__ float load_f32(const void *p, uint64_t i) {
+    if constexpr (TYPE == 0) return __uint_as_float((uint32_t) static_cast<const uint16_t *>(p)[i] << 16);
+    if constexpr (TYPE == 1) return (float)static_cast<const _Float16 *>(p)[i];
+    return static_cast<const float *>(p)[i];
+}
+__device__ __forceinline__ float bf16_to_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+#endif
+
+}  // namespace bsr

@@ -290,6 +290,154 @@ BSR_API int int8_gemm_blockscaled_agroup(const int8_t *a_i8, const int8_t *w_i8,
                                          uint32_t a_group, const float *w_scale, uint16_t *out, uint32_t m,
                                          uint32_t n, uint32_t k, void *stream, int path);
 
+/* ---- expert layers and integer 4-bit weights ------------------------------
+ *
+ * One expert layer over tokens [T]: moe_route picks the experts of each token
+ * and orders the (token, slot) pairs by expert; the products of the rows of
+ * each expert run in int8_grouped_gemm_blockscaled (int8 weights) or
+ * w4a16_group_gemv_experts (4-bit weights, decode); moe_combine adds a token's
+ * rows with their weights (the grouped W8A8 expert product of page
+ * "metrale_model_layers/layers/ops/fp8_moe_grouped_tc_w8a8.rs", with the int8
+ * per-32 formats of this library).
+ *
+ * Rows and experts: the rows [offsets[e], offsets[e + 1]) of a grouped call
+ * belong to expert e.  offsets is a DEVICE array of experts + 1 ascending
+ * int32 values in [0, rows], so no host synchronisation stands between the
+ * router and the products.  It cannot be checked on the host: values outside
+ * [0, rows] are clamped, a descending pair is an expert without rows, and
+ * overlapping ranges leave the shared rows' outputs unspecified; no value
+ * makes a kernel read or write outside its arguments.  Rows outside
+ * [offsets[0], offsets[experts]) are left as they were.
+ */
+
+/* Element types of the arguments that take more than one. */
+enum bsr_type { BSR_TYPE_BF16 = 0, BSR_TYPE_F16 = 1, BSR_TYPE_F32 = 2 };
+
+/* Scores of moe_route. */
+enum bsr_score {
+    BSR_SCORE_SOFTMAX = 0, /* softmax over all experts of the row */
+    BSR_SCORE_SIGMOID = 1  /* sigmoid of each logit               */
+};
+
+/*
+ * Workspace bytes moe_route needs: 0 for few tokens, never more than
+ * 1024 * experts.  Pure host arithmetic, no device call.
+ */
+BSR_API uint64_t moe_route_ws_bytes(uint32_t tokens, uint32_t experts, uint32_t top_k);
+
+/*
+ * Router: the top_k experts of each token, their weights, and the order of
+ * the routed rows by expert.
+ *   logits    [tokens, experts] of `type` (enum bsr_type), rows `ld` elements
+ *             apart (ld >= experts), aligned to the element
+ *   ids       [tokens, top_k] i32  experts by falling logit, ties to the lowest
+ *             index; an expert whose logit is -inf or NaN is never taken, and a
+ *             slot left over (a padded token's row of -inf) holds -1
+ *   weights   [tokens, top_k] f32  scale * score of each id, 0 where it is -1;
+ *             renorm != 0: the scores are divided by their sum over the taken ids
+ *   offsets   [experts + 1] i32    first row of each expert, then the row count
+ *   row_token [tokens * top_k] i32 token of each row; rows of one expert keep
+ *             the order of (token, slot); behind the last row left as it was
+ *   pos       [tokens, top_k] i32  row of each (token, slot), -1 where id is -1
+ *   scale     f32 factor of the weights, finite
+ * Scores are evaluated in binary32, a sum of scores as one binary32 tree;
+ * +inf logits share the softmax between them.  A softmax's maximum is taken
+ * over the row's logits other than NaN.  The result does not depend on the
+ * order in which workgroups run.  tokens == 0 writes offsets (all 0) only.
+ *   workspace 4-byte aligned device buffer of at least moe_route_ws_bytes, as
+ *             that of int8_gemm_blockscaled_ws: scratch, and not shared by
+ *             calls that may overlap in time (NULL where 0 bytes are needed)
+ * Limits: 1 <= experts <= 1024, 1 <= top_k <= min(16, experts), tokens * top_k
+ * < 2^31.
+ * Errors: BSR_EINVAL (those limits, ld, type, score, scale, a workspace that is
+ * too small), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
+ */
+BSR_API int moe_route(const void *logits, int type, uint32_t ld, int32_t *ids, float *weights, int32_t *offsets,
+                      int32_t *row_token, int32_t *pos, uint32_t tokens, uint32_t experts, uint32_t top_k, int score,
+                      int renorm, float scale, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/*
+ * Block-scaled int8 products grouped by expert, ragged row counts:
+ * out[p, j] = bf16_rne( FP32 sum over blocks b of fl32(a_scale[i, b] *
+ * w_scale[e, j, b]) * P[i, e, j, b] ) for the rows p of expert e, with i =
+ * row_index[p] (i = p where row_index is NULL) and P as for
+ * int8_gemm_blockscaled, whose tolerance holds here too.
+ *   a_i8    [a_rows, k]         i8,  16-byte aligned
+ *   w_i8    [experts, n, k]     i8,  16-byte aligned
+ *   a_scale [a_rows, k/32]      f32,  4-byte aligned
+ *   w_scale [experts, n, k/32]  f32,  4-byte aligned
+ *   offsets [experts + 1]       i32,  4-byte aligned (see above)
+ *   row_index [rows] i32 (moe_route's row_token) or NULL; an entry outside
+ *           [0, a_rows) stands for a row of zeros.  NULL needs a_rows >= rows
+ *   out     [rows, n]           BF16 as raw u16, 2-byte aligned
+ * `rows` is the row capacity (tokens * top_k); offsets says how many are used.
+ * Limits: experts <= 65536, rows < 2^31, k < 2^24, and with row_index a_rows *
+ * k < 2^32 (the rows are gathered with 32-bit offsets).
+ * Errors: BSR_EINVAL (k, those limits, a_rows < rows without row_index),
+ * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  rows == 0, n == 0 or
+ * experts == 0 is a valid empty problem.
+ */
+BSR_API int int8_grouped_gemm_blockscaled(const int8_t *a_i8, const int8_t *w_i8, const float *a_scale,
+                                          const float *w_scale, const int32_t *offsets, const int32_t *row_index,
+                                          uint16_t *out, uint32_t a_rows, uint32_t rows, uint32_t experts, uint32_t n,
+                                          uint32_t k, void *stream);
+
+/*
+ * Weighted sum of the experts' rows back into their tokens:
+ * out[t] = bf16_rne( residual[t] + sum over slots s of weights[t, s] *
+ * y[pos[t, s]] ), in binary32, the residual first and the slots in order; a
+ * slot whose pos is outside [0, rows) adds nothing and reads nothing.
+ *   y        [rows, n]       BF16 as raw u16, 2-byte aligned
+ *   pos      [tokens, top_k] i32, weights [tokens, top_k] f32, 4-byte aligned
+ *   residual [tokens, n]     BF16 as raw u16 or NULL, 2-byte aligned
+ *   out      [tokens, n]     BF16 as raw u16, 2-byte aligned; may be residual
+ * Limits: 1 <= top_k <= 16.
+ * Errors: BSR_EINVAL (top_k, more than 2^31 workgroups), BSR_ENULL, BSR_EALIGN,
+ * BSR_EDEVICE, BSR_ELAUNCH.  rows == 0 is valid (no slot adds anything).
+ */
+BSR_API int moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, const uint16_t *residual,
+                        uint16_t *out, uint32_t tokens, uint32_t top_k, uint32_t rows, uint32_t n, void *stream);
+
+/*
+ * Decode GEMV with integer 4-bit weights and a scale (and zero point) per
+ * group of k: out[i, j] = bf16_rne( sum over groups g of scale[j, g] * sum over
+ * k in g of x[i, k] * (c[j, k] - z[j, g]) ), c = 0..15.
+ *   x        [m, k]       BF16 as raw u16, 16-byte aligned
+ *   w_packed [n, k/2]     u8, two codes per byte, element 2j in the LOW nibble
+ *                         of byte j; 16-byte aligned
+ *   scale    [n, k/group] of scale_type (enum bsr_type), aligned to the element
+ *   zero     [n, k/group] u8 zero points 0..255, or NULL: every z is 8
+ *   group    32, 64 or 128 (dividing k), or 0: one scale per row of the weight
+ *   out      [m, n]       BF16 as raw u16, 2-byte aligned
+ * Evaluated in binary32: per group the codes enter as the exact values 16 + c
+ * and (16 + z) * sum(x) is taken off, then the scale is applied once, so the
+ * error of a sum is bounded with the terms |x| * scale * (32 + c + z).
+ * Meant for m <= 16; every further 16 rows read the weight once more.
+ * Errors: BSR_EINVAL (k, group, scale_type, more than 2^31 workgroups),
+ * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
+ */
+BSR_API int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type,
+                             const uint8_t *zero, uint32_t group, uint16_t *out, uint32_t m, uint32_t n, uint32_t k,
+                             void *stream);
+
+/*
+ * w4a16_group_gemv by expert: row p of expert e takes the weight of e.
+ *   x        [x_rows, k]           w_packed [experts, n, k/2]
+ *   scale    [experts, n, k/group] zero     [experts, n, k/group] or NULL
+ *   offsets, row_index as int8_grouped_gemm_blockscaled
+ *   silu_mul 0: out [rows, n].  1: columns 0..n/2-1 of the weight are the gate
+ *            and n/2..n-1 the up projection, out [rows, n/2] =
+ *            bf16_rne( fl32(gate / fl32(1 + exp(-gate))) * up ), gate and up in
+ *            binary32; n must be even
+ * Limits: experts <= 65536, rows < 2^31.
+ * Errors: as w4a16_group_gemv; BSR_EINVAL too for x_rows < rows without
+ * row_index, silu_mul other than 0 or 1, an odd n with it, and those limits.
+ */
+BSR_API int w4a16_group_gemv_experts(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type,
+                                     const uint8_t *zero, uint32_t group, const int32_t *offsets,
+                                     const int32_t *row_index, int silu_mul, uint16_t *out, uint32_t x_rows,
+                                     uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 BSR_API const char *bsr_status_string(int status);
 
