@@ -5,61 +5,68 @@
 // operand row i = row_index[p] (the grouped W8A8 expert product of page
 // "metrale_model_layers/layers/ops/fp8_moe_grouped_tc_w8a8.rs").
 //
-// A workgroup takes 16 rows of one expert and 64 columns, a wave 16 of them;
-// per 32-wide block one v_mfma_i32_16x16x32_i8 gives the exact P.
+// The offsets are device values, so the host launches as many workgroups as
+// any offsets could need and each finds its tile itself: a lane per expert
+// counts row tiles, a wave prefix gives their total and the tile of this
+// workgroup; workgroups past the total leave.  The tiles are those of
+// gemm_tile.h, their A rows gathered through row_index by the staging itself,
+// so no gathered copy of the activations is made.
+#include "gemm_tile.h"
 #include "moe_internal.h"
 
 namespace bsr {
-namespace {
+namespace gemm_kernels {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-
-constexpr uint32_t kRows = 16, kCols = 64;
-
-__global__ __launch_bounds__(256) void grouped_gemm_kernel(const int8_t *__restrict__ a, const int8_t *__restrict__ w,
-                                                           const float *__restrict__ a_s,
-                                                           const float *__restrict__ w_s, uint16_t *__restrict__ out,
-                                                           GroupedRows g, uint32_t n, uint32_t k, uint32_t col_tiles) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const RowTile t = find_row_tile(g, kRows, blockIdx.x / col_tiles, lane);
-    if (t.rows == 0) return;
-    const uint32_t c = lane & 15, q = lane >> 4;
-    const uint32_t col = (blockIdx.x % col_tiles) * kCols + wave * 16 + c;
-    const uint32_t nb = k / 32;
-    const uint64_t wrow = (uint64_t)t.expert * n + min(col, n - 1);
-    const int32_t src = c < t.rows ? source_row(g, t.row0 + c) : -1;
-    const int8_t *wp = w + wrow * k + 8 * q;
-    const float *wsp = w_s + wrow * nb;
-    const int8_t *ap = a + (uint64_t)max(src, 0) * k + 8 * q;
-    int32_t srow[4];  // this lane's output rows 4 q + r
-#pragma unroll
-    for (int r = 0; r < 4; ++r) srow[r] = 4 * q + r < t.rows ? source_row(g, t.row0 + 4 * q + r) : -1;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t b = 0; b < nb; ++b) {
-        const long av = *reinterpret_cast<const long *>(ap + 32 * (uint64_t)b);
-        const long wv = *reinterpret_cast<const long *>(wp + 32 * (uint64_t)b);
-        const v4i p = __builtin_amdgcn_mfma_i32_16x16x32_i8(src < 0 ? 0 : av, wv, v4i{0, 0, 0, 0}, 0, 0, 0);
-        const float ws = wsp[b];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float as = srow[r] < 0 ? 0.0f : a_s[(uint64_t)srow[r] * nb + b];
-            acc[r] = fmaf((float)p[r], as * ws, acc[r]);
-        }
+template <int BM, int BN, int WM, int WN, int WG_PER_CU, int RING, bool GATHER>
+__global__ __launch_bounds__(BM * BN / (WM * WN) * 64, WG_PER_CU) void grouped_kernel(
+    const int8_t *__restrict__ a, const int8_t *__restrict__ w, const float *__restrict__ a_s,
+    const float *__restrict__ w_s, uint16_t *__restrict__ out, GroupedRows g, uint32_t N, uint32_t K,
+    uint32_t tiles_n) {
+    RowTiles rt(g, BM, threadIdx.x & 63);
+    const uint64_t tiles_m = rt.count();
+    if (blockIdx.x >= tiles_m * tiles_n) return;
+    uint32_t tm, tn;
+    tile_of<BM == kGemmTallBM ? kGemmTallGroupM : kGemmGroupM>(
+        blockIdx.x, (uint32_t)min(tiles_m, (uint64_t)(gridDim.x / tiles_n)), tiles_n, tm, tn);
+    const RowTile r = rt.find(tm);
+    if (r.rows == 0) return;
+    const uint32_t n0 = tn * BN, nb = K / 32;
+    const uint64_t wrow = (uint64_t)r.expert * N + n0;
+    TileArgs t = {a, w + wrow * K, a_s, w_s + wrow * nb, nullptr, r.rows, min((uint32_t)BN, N - n0), 0,
+                  r.row0, n0, r.row0 + r.rows};
+    if constexpr (GATHER) {
+        t.index = g.index + r.row0;
+        t.buf_rows = g.src_rows;
+    } else {
+        t.a += (uint64_t)r.row0 * K;
+        t.a_s += (uint64_t)r.row0 * nb;
+        t.buf_rows = r.rows;
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (4 * q + r < t.rows && col < n) out[(uint64_t)(t.row0 + 4 * q + r) * n + col] = f32_to_bf16_rne(acc[r]);
+    gemm_tile<BM, BN, WM, WN, 1, RING, false, GATHER>(t, out, N, K, nb, 0, nullptr, 0, 0, 0);
 }
 
-}  // namespace
+template <int BM, int BN, int WM, int WN, int WG_PER_CU, int RING>
+hipError_t launch_grouped(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
+                          const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s) {
+    const uint32_t tiles_n = (uint32_t)div_up(n, BN);
+    const uint64_t grid = grouped_row_tiles(g.rows, g.experts, BM) * tiles_n;
+    auto kernel = g.index != nullptr ? grouped_kernel<BM, BN, WM, WN, WG_PER_CU, RING, true>
+                                     : grouped_kernel<BM, BN, WM, WN, WG_PER_CU, RING, false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(Geo<BM, BN, WM, WN>::kThreads), 0, s, a, w, a_s, w_s, out, g,
+                       n, k, tiles_n);
+    return hipGetLastError();
+}
+
+}  // namespace gemm_kernels
 
 hipError_t launch_grouped_gemm(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
                                const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s) {
-    const uint32_t col_tiles = (uint32_t)div_up(n, kCols);
-    const uint64_t grid = grouped_row_tiles(g.rows, g.experts, kRows) * col_tiles;
-    hipLaunchKernelGGL(grouped_gemm_kernel, dim3((uint32_t)grid), dim3(256), 0, s, a, w, a_s, w_s, out, g, n, k,
-                       col_tiles);
-    return hipGetLastError();
+    using namespace gemm_kernels;
+    const uint32_t used = g.rows < g.experts ? g.rows : g.experts;
+    const uint32_t mean = g.rows / used;
+    if (mean >= 192) return launch_grouped<kGemmTallBM, kGemmBN, 64, 64, 1, 2>(a, w, a_s, w_s, out, g, n, k, s);
+    if (mean >= 64) return launch_grouped<kGemmBM, kGemmBN, 64, 64, 2, 2>(a, w, a_s, w_s, out, g, n, k, s);
+    return launch_grouped<kGemmSmallTile, kGemmSmallTile, 32, 32, 2, 4>(a, w, a_s, w_s, out, g, n, k, s);
 }
 
 }  // namespace bsr

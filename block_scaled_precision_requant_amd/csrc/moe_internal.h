@@ -35,41 +35,68 @@ struct RowTile {
     uint32_t expert, row0, rows;  // rows == 0: no such tile
 };
 
-// Row tile v of tiles of bm rows.  Every lane of the wave must be active; the
-// result is the same in all of them.  offsets come from the device unchecked,
-// so each range is clamped to [0, rows].
-__device__ __forceinline__ RowTile find_row_tile(const GroupedRows &g, uint32_t bm, uint32_t v, int lane) {
-    if (g.offsets == nullptr) {
-        const uint32_t row0 = v * bm;
-        return {0, row0, row0 < g.rows ? min(bm, g.rows - row0) : 0};
+// The experts' rows in tiles of bm rows, none across two experts: how many
+// there are, and which rows the v-th is.  Every lane of the wave must be
+// active; results are the same in all of them.  offsets come from the device
+// unchecked, so each range is clamped to [0, rows].  A lane holds one of 64
+// experts at a time (of the only 64 from construction on, where they suffice).
+struct RowTiles {
+    const GroupedRows &g;
+    uint32_t bm;
+    int lane;
+    uint32_t lo, hi, incl, tiles;  // this lane's expert: rows, tiles and their inclusive prefix
+
+    __device__ __forceinline__ RowTiles(const GroupedRows &g_, uint32_t bm_, int lane_) : g(g_), bm(bm_), lane(lane_) {
+        if (g.offsets != nullptr) load(0);
     }
-    uint32_t before = 0;  // tiles of the experts already passed
-    for (uint32_t e0 = 0; e0 < g.experts; e0 += 64) {
+    __device__ __forceinline__ void load(uint32_t e0) {
         const uint32_t e = e0 + lane;
-        uint32_t lo = 0, hi = 0;
+        lo = hi = 0;
         if (e < g.experts) {
             lo = (uint32_t)min(max(g.offsets[e], 0), (int32_t)g.rows);
             hi = (uint32_t)min(max(g.offsets[e + 1], (int32_t)lo), (int32_t)g.rows);
         }
-        const uint32_t tiles = (hi - lo + bm - 1) / bm;
-        uint32_t incl = tiles;
+        tiles = (hi - lo + bm - 1) / bm;
+        incl = tiles;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t o = __shfl_up(incl, d);
             if (lane >= d) incl += o;
         }
-        const uint64_t past = __ballot(before + incl > v);
-        if (past != 0) {
-            const int owner = __builtin_ctzll(past);
-            const uint32_t first = before + __builtin_amdgcn_readlane(incl - tiles, owner);
-            const uint32_t olo = __builtin_amdgcn_readlane(lo, owner), ohi = __builtin_amdgcn_readlane(hi, owner);
-            const uint32_t row0 = olo + (v - first) * bm;
-            return {e0 + owner, row0, min(bm, ohi - row0)};
-        }
-        before += __builtin_amdgcn_readlane(incl, 63);
     }
-    return {0, 0, 0};
-}
+    // Sums past the grid's bound (overlapping ranges) stop at 2^30 tiles per 64
+    // experts at most: ranges end at rows < 2^31 and the callers cut at the grid.
+    __device__ __forceinline__ uint64_t count() {
+        if (g.offsets == nullptr) return (g.rows + bm - 1) / bm;
+        uint64_t n = __builtin_amdgcn_readlane(incl, 63);
+        for (uint32_t e0 = 64; e0 < g.experts; e0 += 64) {
+            load(e0);
+            n += __builtin_amdgcn_readlane(incl, 63);
+        }
+        if (g.experts > 64) load(0);
+        return n;
+    }
+    __device__ __forceinline__ RowTile find(uint32_t v) {
+        if (g.offsets == nullptr) {
+            const uint32_t row0 = v * bm;
+            return {0, row0, row0 < g.rows ? min(bm, g.rows - row0) : 0};
+        }
+        for (uint32_t e0 = 0;;) {
+            const uint64_t past = __ballot(incl > v);
+            if (past != 0) {
+                const int owner = __builtin_ctzll(past);
+                const uint32_t first = __builtin_amdgcn_readlane(incl - tiles, owner);
+                const uint32_t olo = __builtin_amdgcn_readlane(lo, owner), ohi = __builtin_amdgcn_readlane(hi, owner);
+                const uint32_t row0 = olo + (v - first) * bm;
+                return {e0 + owner, row0, min(bm, ohi - row0)};
+            }
+            v -= __builtin_amdgcn_readlane(incl, 63);
+            e0 += 64;
+            if (e0 >= g.experts) return {0, 0, 0};
+            load(e0);
+        }
+    }
+};
 
 // Operand row of output row p, or -1 for a row of zeros.
 __device__ __forceinline__ int32_t source_row(const GroupedRows &g, uint32_t p) {

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void w4_group_kernel(const uint16_t *__restric
                                                        uint16_t *__restrict__ out, GroupedRows g, uint32_t n,
                                                        uint32_t k, uint32_t col_tiles, bool silu) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const RowTile t = find_row_tile(g, kRows, blockIdx.x / col_tiles, lane);
+    const RowTile t = RowTiles(g, kRows, lane).find(blockIdx.x / col_tiles);
     if (t.rows == 0) return;
     const uint32_t c = lane & 15, q = lane >> 4;
     const uint32_t cols = silu ? n / 2 : n;
