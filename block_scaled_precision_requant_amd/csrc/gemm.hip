@@ -29,7 +29,8 @@ __global__ __launch_bounds__(BM * BN / (WM * WN) * 64 * KG, WG_PER_CU) void gemm
     const uint32_t rows_a = min((uint32_t)BM, M - m0);
     const TileArgs t = {a + (uint64_t)m0 * K, w + (uint64_t)n0 * K, a_s + (uint64_t)m0 * a_ld,
                         w_s + (uint64_t)n0 * (K / 32), nullptr, rows_a, min((uint32_t)BN, N - n0), rows_a, m0, n0, M};
-    gemm_tile<BM, BN, WM, WN, KG, RING, SPLIT, false>(t, out, N, K, a_ld, a_shift, partial, pitch, slice, slice_stages);
+    __shared__ __attribute__((aligned(1024))) char lds[TileTraits<BM, BN, WM, WN, KG, RING, SPLIT>::kLds];
+    gemm_tile<BM, BN, WM, WN, KG, RING, SPLIT, false>(lds, t, out, N, K, a_ld, a_shift, partial, pitch, slice, slice_stages);
 }
 
 // The K slices of a split GEMM: out = bf16_rne(((p_0 + p_1) + p_2) + ...), the

@@ -371,6 +371,26 @@ struct TileArgs {
     uint32_t out_row, out_col, row_end;  // first output row and column; rows from row_end on are not the tile's
 };
 
+// kSc8 -- the 256 x 128 and 128 x 128 shapes with a ring of 2 and the 64 x 64
+// shape with a ring of 4 (K split or not): operands in RING OpStage buffers, scales in
+// Sc8Stage buffers of 8 blocks (2 for a ring of 2; 3 for a ring of 4,
+// whose copies run three stages ahead), and each stage's copies spread
+// over the units that compute the stage before them.
+// kLds: the LDS bytes of a tile (aligned to 1024).
+template <int BM, int BN, int WM, int WN, int KG, int RING, bool SPLIT>
+struct TileTraits {
+    using G = Geo<BM, BN, WM, WN>;
+    static constexpr bool kSc8 =
+        (RING == 2 && KG == 1 && !SPLIT && (BM == 128 || BM == kGemmTallBM) && BN == 128) ||
+        (RING == 4 && KG == 1 && BM == 64 && BN == 64);
+    static constexpr int kScBufs = RING == 2 ? 2 : 3;
+    // units that carry the copies: a ring of 2 leaves the copies one stage to
+    // land, so only the first pair's units carry them; a ring of 4, all units
+    static constexpr int kSpreadUnits = RING == 2 ? 2 * G::kTM * G::kTN : 4 * G::kTM * G::kTN;
+    static constexpr size_t kLds = kSc8 ? RING * sizeof(OpStage<BM, BN>) + kScBufs * sizeof(Sc8Stage<BM, BN>)
+                                        : sizeof(Stage<BM, BN>) * KG * RING;
+};
+
 // KG: K groups.  With KG > 1 the workgroup holds KG copies of the wave grid,
 // each with its own ring, walking its own contiguous range of stages; at the
 // end the groups' FP32 tiles are added in group order through LDS.  This
@@ -383,28 +403,19 @@ struct TileArgs {
 // added in slice order by split_reduce_kernel.
 // GATHER: the tile's A rows are picked by index.
 template <int BM, int BN, int WM, int WN, int KG, int RING, bool SPLIT, bool GATHER>
-__device__ __forceinline__ void gemm_tile(const TileArgs &ta, uint16_t *__restrict__ out, uint32_t N, uint32_t K,
+__device__ __forceinline__ void gemm_tile(char *lds, const TileArgs &ta, uint16_t *__restrict__ out, uint32_t N, uint32_t K,
                                           uint32_t a_ld, uint32_t a_shift, float *__restrict__ partial, uint64_t pitch,
                                           uint32_t slice, uint32_t slice_stages) {
     static_assert(!(SPLIT && KG > 1), "one K split at a time");
     using G = Geo<BM, BN, WM, WN>;
     constexpr int TM = G::kTM, TN = G::kTN;
     using St = Stage<BM, BN>;
-    // kSc8 -- the 256 x 128 and 128 x 128 shapes with a ring of 2 and the 64 x 64
-    // shape with a ring of 4 (K split or not): operands in RING OpStage buffers, scales in
-    // Sc8Stage buffers of 8 blocks (2 for a ring of 2; 3 for a ring of 4,
-    // whose copies run three stages ahead), and each stage's copies spread
-    // over the units that compute the stage before them.
-    constexpr bool kSc8 = (RING == 2 && KG == 1 && !SPLIT && (BM == 128 || BM == kGemmTallBM) && BN == 128) ||
-                          (RING == 4 && KG == 1 && BM == 64 && BN == 64);
-    constexpr int kScBufs = RING == 2 ? 2 : 3;
-    // units that carry the copies: a ring of 2 leaves the copies one stage to
-    // land, so only the first pair's units carry them; a ring of 4, all units
-    constexpr int kSpreadUnits = RING == 2 ? 2 * TM * TN : 4 * TM * TN;
+    using T = TileTraits<BM, BN, WM, WN, KG, RING, SPLIT>;
+    constexpr bool kSc8 = T::kSc8;
+    constexpr int kScBufs = T::kScBufs, kSpreadUnits = T::kSpreadUnits;
     using Op = OpStage<BM, BN>;
     using Sc = Sc8Stage<BM, BN>;
-    constexpr size_t kLds = kSc8 ? RING * sizeof(Op) + kScBufs * sizeof(Sc) : sizeof(St) * KG * RING;
-    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    constexpr size_t kLds = T::kLds;
     St(*rings)[RING] = reinterpret_cast<St(*)[RING]>(lds);
     Op *ops = reinterpret_cast<Op *>(lds);
     Sc *scs = reinterpret_cast<Sc *>(lds + RING * sizeof(Op));

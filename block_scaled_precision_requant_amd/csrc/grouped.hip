@@ -7,7 +7,7 @@
 //
 // The offsets are device values, so the host launches as many workgroups as
 // any offsets could need and each finds its tile itself: a lane per expert
-// counts row tiles, a wave prefix gives their total and the tile of this
+// counts row tiles, wave prefixes give their totals and the tile of this
 // workgroup; workgroups past the total leave.  The tiles are those of
 // gemm_tile.h, their A rows gathered through row_index by the staging itself,
 // so no gathered copy of the activations is made.
@@ -17,56 +17,152 @@
 namespace bsr {
 namespace gemm_kernels {
 
-template <int BM, int BN, int WM, int WN, int WG_PER_CU, int RING, bool GATHER>
-__global__ __launch_bounds__(BM * BN / (WM * WN) * 64, WG_PER_CU) void grouped_kernel(
+// Row tiles of kGemmBM rows in falling order of work: first those of more than
+// 64 rows (class 0), then an expert's last 33..64 rows (1), then last 1..32 (2).
+struct ClassedTiles {
+    GroupedRows g;
+    int lane;
+    uint32_t lo, hi;       // rows of this lane's expert
+    uint32_t full, full_incl, last_incl;  // its tiles of class 0, and the inclusive prefixes over the lanes: of
+                                          // class 0, and of 1 (low half) and 2 (at most one each per expert)
+    uint32_t n0, n1, n2;   // tiles of each class
+
+    __device__ __forceinline__ ClassedTiles(const GroupedRows &g_, int lane_) : g(g_), lane(lane_), n0(0), n1(0), n2(0) {
+        for (uint32_t e0 = 0; e0 < g.experts; e0 += 64) {
+            load(e0);
+            const uint32_t both = __builtin_amdgcn_readlane(last_incl, 63);
+            n0 += __builtin_amdgcn_readlane(full_incl, 63);
+            n1 += both & 0xFFFFu;
+            n2 += both >> 16;
+        }
+        if (g.experts > 64) load(0);
+    }
+    __device__ __forceinline__ void load(uint32_t e0) {
+        g.range(e0 + lane, lo, hi);
+        const uint32_t last = (hi - lo) % kGemmBM;
+        full = (hi - lo) / kGemmBM + (last > 64);
+        full_incl = full;
+        last_incl = (last > 32 && last <= 64 ? 1u : 0u) | (last > 0 && last <= 32 ? 1u << 16 : 0u);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t x = __shfl_up(full_incl, d), y = __shfl_up(last_incl, d);
+            if (lane >= d) {
+                full_incl += x;
+                last_incl += y;
+            }
+        }
+    }
+    __device__ __forceinline__ RowTile find(uint32_t v) {
+        const bool whole = v < n0;
+        const uint32_t shift = v < n0 + n1 ? 0 : 16;
+        v -= whole ? 0 : (shift == 0 ? n0 : n0 + n1);
+        for (uint32_t e0 = 0;;) {
+            const uint32_t part = (last_incl >> shift) & 0xFFFFu;
+            const uint32_t incl = whole ? full_incl : part;
+            const uint64_t past = __ballot(incl > v);
+            if (past != 0) {
+                const int o = __builtin_ctzll(past);
+                const uint32_t olo = __builtin_amdgcn_readlane(lo, o), ohi = __builtin_amdgcn_readlane(hi, o);
+                const uint32_t first = __builtin_amdgcn_readlane(incl - full, o);
+                const uint32_t row0 = whole ? olo + (v - first) * kGemmBM : ohi - (ohi - olo) % kGemmBM;
+                return {e0 + o, row0, min((uint32_t)kGemmBM, ohi - row0)};
+            }
+            v -= __builtin_amdgcn_readlane(incl, 63);
+            e0 += 64;
+            if (e0 >= g.experts) return {0, 0, 0};
+            load(e0);
+        }
+    }
+};
+
+// Workgroup -> (row tile, column tile).  Tiles are walked in groups of
+// kGemmGroupM row tiles, down the rows first; each XCD takes runs of kRun
+// consecutive tiles in turn, so that a run shares A and W rows in the XCD's L2
+// while the work of every part of the list is spread over all XCDs (one run
+// per XCD, as the dense GEMM has it, gives some XCDs the full tiles and others
+// the experts' remainders).
+#ifndef RUN
+#define RUN 64
+#endif
+constexpr uint32_t kRun = RUN;
+__device__ __forceinline__ void grouped_tile_of(uint32_t wg, uint32_t tiles_m, uint32_t tiles_n, uint32_t &tm,
+                                                uint32_t &tn) {
+    const uint32_t total = tiles_m * tiles_n, whole = total / (kXcds * kRun);
+    const uint32_t x = wg % kXcds, j = wg / kXcds;
+    uint32_t v;
+    if (j / kRun < whole) {
+        v = (j / kRun * kXcds + x) * kRun + j % kRun;
+    } else {
+        const uint32_t left = total - whole * kXcds * kRun, q = left / kXcds, r = left % kXcds;
+        v = whole * kXcds * kRun + x * q + min(x, r) + (j - whole * kRun);
+    }
+    const uint32_t per_group = kGemmGroupM * tiles_n;
+    const uint32_t first_m = v / per_group * kGemmGroupM;
+    const uint32_t gsize = min(tiles_m - first_m, (uint32_t)kGemmGroupM);
+    tm = first_m + v % per_group % gsize;
+    tn = v % per_group / gsize;
+}
+
+// One tile of up to 128 x 128 outputs, four waves of 64 x 64, two workgroups
+// per CU.  An expert's last rows, when 64 or 32 hold them, take a wave grid that computes
+// no more than that: each of the four waves 64 x 32 or 32 x 32.
+template <bool GATHER>
+__global__ __launch_bounds__(256, 2) void grouped_kernel(
     const int8_t *__restrict__ a, const int8_t *__restrict__ w, const float *__restrict__ a_s,
     const float *__restrict__ w_s, uint16_t *__restrict__ out, GroupedRows g, uint32_t N, uint32_t K,
     uint32_t tiles_n) {
-    RowTiles rt(g, BM, threadIdx.x & 63);
-    const uint64_t tiles_m = rt.count();
+    constexpr int BM = kGemmBM, BN = kGemmBN;
+    __shared__ __attribute__((aligned(1024))) char lds[TileTraits<BM, BN, 64, 64, 1, 2, false>::kLds];
+    ClassedTiles rt(g, threadIdx.x & 63);
+    // (overlapping ranges could ask for more tiles than the grid has: those are not computed)
+    const uint32_t tiles_m = min(rt.n0 + rt.n1 + rt.n2, gridDim.x / tiles_n);
     if (blockIdx.x >= tiles_m * tiles_n) return;
     uint32_t tm, tn;
-    tile_of<BM == kGemmTallBM ? kGemmTallGroupM : kGemmGroupM>(
-        blockIdx.x, (uint32_t)min(tiles_m, (uint64_t)(gridDim.x / tiles_n)), tiles_n, tm, tn);
-    const RowTile r = rt.find(tm);
+#ifdef CONTIG
+    tile_of<kGemmGroupM>(blockIdx.x, tiles_m, tiles_n, tm, tn);
+#else
+#ifdef CONTIG
+    tile_of<kGemmGroupM>(blockIdx.x, tiles_m, tiles_n, tm, tn);
+#else
+    grouped_tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+#endif
+#endif
+    RowTile r = rt.find(tm);
+    // the same in every lane; said so, since a buffer descriptor that the compiler
+    // takes for a vector costs a loop around each copy
+    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
+    r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
+    r.rows = __builtin_amdgcn_readfirstlane(r.rows);
     if (r.rows == 0) return;
-    const uint32_t n0 = tn * BN, nb = K / 32;
+    const uint32_t n0 = __builtin_amdgcn_readfirstlane(tn * BN), nb = K / 32;
     const uint64_t wrow = (uint64_t)r.expert * N + n0;
     TileArgs t = {a, w + wrow * K, a_s, w_s + wrow * nb, nullptr, r.rows, min((uint32_t)BN, N - n0), 0,
                   r.row0, n0, r.row0 + r.rows};
     if constexpr (GATHER) {
         t.index = g.index + r.row0;
-        t.buf_rows = g.src_rows;
+        t.buf_rows = __builtin_amdgcn_readfirstlane(g.src_rows);
     } else {
         t.a += (uint64_t)r.row0 * K;
         t.a_s += (uint64_t)r.row0 * nb;
         t.buf_rows = r.rows;
     }
-    gemm_tile<BM, BN, WM, WN, 1, RING, false, GATHER>(t, out, N, K, nb, 0, nullptr, 0, 0, 0);
-}
-
-template <int BM, int BN, int WM, int WN, int WG_PER_CU, int RING>
-hipError_t launch_grouped(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
-                          const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s) {
-    const uint32_t tiles_n = (uint32_t)div_up(n, BN);
-    const uint64_t grid = grouped_row_tiles(g.rows, g.experts, BM) * tiles_n;
-    auto kernel = g.index != nullptr ? grouped_kernel<BM, BN, WM, WN, WG_PER_CU, RING, true>
-                                     : grouped_kernel<BM, BN, WM, WN, WG_PER_CU, RING, false>;
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(Geo<BM, BN, WM, WN>::kThreads), 0, s, a, w, a_s, w_s, out, g,
-                       n, k, tiles_n);
-    return hipGetLastError();
+    if (r.rows <= 32)
+        gemm_tile<32, BN, 32, 32, 1, 2, false, GATHER>(lds, t, out, N, K, nb, 0, nullptr, 0, 0, 0);
+    else if (r.rows <= 64)
+        gemm_tile<64, BN, 64, 32, 1, 2, false, GATHER>(lds, t, out, N, K, nb, 0, nullptr, 0, 0, 0);
+    else
+        gemm_tile<BM, BN, 64, 64, 1, 2, false, GATHER>(lds, t, out, N, K, nb, 0, nullptr, 0, 0, 0);
 }
 
 }  // namespace gemm_kernels
 
 hipError_t launch_grouped_gemm(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
                                const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s) {
-    using namespace gemm_kernels;
-    const uint32_t used = g.rows < g.experts ? g.rows : g.experts;
-    const uint32_t mean = g.rows / used;
-    if (mean >= 192) return launch_grouped<kGemmTallBM, kGemmBN, 64, 64, 1, 2>(a, w, a_s, w_s, out, g, n, k, s);
-    if (mean >= 64) return launch_grouped<kGemmBM, kGemmBN, 64, 64, 2, 2>(a, w, a_s, w_s, out, g, n, k, s);
-    return launch_grouped<kGemmSmallTile, kGemmSmallTile, 32, 32, 2, 4>(a, w, a_s, w_s, out, g, n, k, s);
+    const uint32_t tiles_n = (uint32_t)div_up(n, kGemmBN);
+    const uint64_t grid = grouped_row_tiles(g.rows, g.experts, kGemmBM) * tiles_n;
+    auto kernel = g.index != nullptr ? gemm_kernels::grouped_kernel<true> : gemm_kernels::grouped_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(256), 0, s, a, w, a_s, w_s, out, g, n, k, tiles_n);
+    return hipGetLastError();
 }
 
 }  // namespace bsr

@@ -22,6 +22,18 @@ struct GroupedRows {
     const int32_t *offsets;
     const int32_t *index;
     uint32_t src_rows, rows, experts;
+
+#ifdef __HIPCC__
+    // Rows of expert e, empty past the last expert.  The offsets come from the
+    // device unchecked: clamped to [0, rows], a descending pair is empty.
+    __device__ __forceinline__ void range(uint32_t e, uint32_t &lo, uint32_t &hi) const {
+        lo = hi = 0;
+        if (e < experts) {
+            lo = (uint32_t)min(max(offsets[e], 0), (int32_t)rows);
+            hi = (uint32_t)min(max(offsets[e + 1], (int32_t)lo), (int32_t)rows);
+        }
+    }
+#endif
 };
 
 hipError_t launch_grouped_gemm(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
@@ -35,13 +47,11 @@ struct RowTile {
     uint32_t expert, row0, rows;  // rows == 0: no such tile
 };
 
-// The experts' rows in tiles of bm rows, none across two experts: how many
-// there are, and which rows the v-th is.  Every lane of the wave must be
-// active; results are the same in all of them.  offsets come from the device
-// unchecked, so each range is clamped to [0, rows].  A lane holds one of 64
-// experts at a time (of the only 64 from construction on, where they suffice).
+// The experts' rows in tiles of bm rows, none across two experts: which rows
+// the v-th is.  Every lane of the wave must be active; the result is the same
+// in all of them.  A lane holds one of 64 experts at a time.
 struct RowTiles {
-    const GroupedRows &g;
+    GroupedRows g;
     uint32_t bm;
     int lane;
     uint32_t lo, hi, incl, tiles;  // this lane's expert: rows, tiles and their inclusive prefix
@@ -50,12 +60,7 @@ struct RowTiles {
         if (g.offsets != nullptr) load(0);
     }
     __device__ __forceinline__ void load(uint32_t e0) {
-        const uint32_t e = e0 + lane;
-        lo = hi = 0;
-        if (e < g.experts) {
-            lo = (uint32_t)min(max(g.offsets[e], 0), (int32_t)g.rows);
-            hi = (uint32_t)min(max(g.offsets[e + 1], (int32_t)lo), (int32_t)g.rows);
-        }
+        g.range(e0 + lane, lo, hi);
         tiles = (hi - lo + bm - 1) / bm;
         incl = tiles;
 #pragma unroll
@@ -63,18 +68,6 @@ struct RowTiles {
             const uint32_t o = __shfl_up(incl, d);
             if (lane >= d) incl += o;
         }
-    }
-    // Sums past the grid's bound (overlapping ranges) stop at 2^30 tiles per 64
-    // experts at most: ranges end at rows < 2^31 and the callers cut at the grid.
-    __device__ __forceinline__ uint64_t count() {
-        if (g.offsets == nullptr) return (g.rows + bm - 1) / bm;
-        uint64_t n = __builtin_amdgcn_readlane(incl, 63);
-        for (uint32_t e0 = 64; e0 < g.experts; e0 += 64) {
-            load(e0);
-            n += __builtin_amdgcn_readlane(incl, 63);
-        }
-        if (g.experts > 64) load(0);
-        return n;
     }
     __device__ __forceinline__ RowTile find(uint32_t v) {
         if (g.offsets == nullptr) {
