@@ -91,14 +91,17 @@ def _stream(stream, like):
 # E4M3), 16-bit BF16 bits (any 2-byte dtype: torch.bfloat16, int16, uint16)
 # and binary32 scales.
 BYTES, BF16, F32, I32 = "1-byte", "2-byte", "float32", "int32"
+_USUAL = {BYTES: {torch.int8, torch.uint8}, BF16: {torch.bfloat16, torch.int16}, F32: {torch.float32},
+          I32: {torch.int32}}  # what _kind need not look at
 
 
 def _shape(t, shape, what, kind):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    _kind(t, what, kind)
+    if t.dtype not in _USUAL[kind]:
+        _kind(t, what, kind)
 
 
 def _kind(t, what, kind):
@@ -296,16 +299,29 @@ def _type(t, what):
 
 
 def _launch(name, stream, tensors, args):
-    """Calls an entry point with the tensors' device as the current one, on `stream`
-    (default: torch's current stream there)."""
-    dev = tensors[0].device
+    """Calls an entry point with the data pointers of `tensors` (None: NULL), the other arguments and a stream
+    (default: torch's current one on the tensors' device), that device being the current one during the call.
+    Small decode calls last as long as this does, so it takes the short ways: integers for devices and pointers."""
+    dev = tensors[0].get_device()
+    ptrs = []
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"arguments on {dev} and {t.device}: all must be on one device")
-    if dev.type != "cuda":
+        if t is None:
+            ptrs.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"arguments on {tensors[0].device} and {t.device}: all must be on one device")
+        ptrs.append(t.data_ptr())
+    if dev < 0:
         raise ValueError("arguments must be device tensors")
-    with torch.cuda.device(dev):
-        _done(getattr(lib(), name)(*args, _stream(stream, tensors[0])), name)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    fn = getattr(_LIB or lib(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args(ptrs), raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args(ptrs), raw)
+    if status != BSR_OK:
+        raise BsrError(status, name)
 
 
 def moe_route_ws_bytes(tokens, experts, top_k):
@@ -332,10 +348,9 @@ def moe_route(logits, ids, weights, offsets, row_token, pos, workspace=None, sco
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: must be contiguous")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch("moe_route", stream, (offsets, logits, ids, weights, row_token, pos, workspace),
-            (_ptr(logits), kind, logits.stride(0) if t > 1 else e, _ptr(ids), _ptr(weights), _ptr(offsets),
-             _ptr(row_token), _ptr(pos), t, e, k, int(score), int(bool(renorm)), float(scale), _ptr(workspace),
-             ws_bytes))
+    ld = logits.stride(0) if t > 1 else e
+    _launch("moe_route", stream, (logits, ids, weights, offsets, row_token, pos, workspace),
+            lambda p: (p[0], kind, ld, *p[1:6], t, e, k, int(score), int(bool(renorm)), float(scale), p[6], ws_bytes))
 
 
 def _grouped_shapes(offsets, row_index, out, cols, experts):
@@ -357,9 +372,8 @@ def int8_grouped_gemm_blockscaled(a_i8, w_i8, a_scale, w_scale, offsets, out, ro
     _shape(a_scale, (a_rows, k // 32), "a_scale", F32)
     _shape(w_scale, (e, n, k // 32), "w_scale", F32)
     rows = _grouped_shapes(offsets, row_index, out, n, e)
-    _launch("int8_grouped_gemm_blockscaled", stream, (out, a_i8, w_i8, a_scale, w_scale, offsets, row_index),
-            (_ptr(a_i8), _ptr(w_i8), _ptr(a_scale), _ptr(w_scale), _ptr(offsets), _ptr(row_index), _ptr(out), a_rows,
-             rows, e, n, k))
+    _launch("int8_grouped_gemm_blockscaled", stream, (a_i8, w_i8, a_scale, w_scale, offsets, row_index, out),
+            lambda p: (*p, a_rows, rows, e, n, k))
 
 
 def moe_combine(y, pos, weights, out, residual=None, stream=None):
@@ -373,21 +387,20 @@ def moe_combine(y, pos, weights, out, residual=None, stream=None):
     _shape(out, (t, n), "out", BF16)
     if residual is not None:
         _shape(residual, (t, n), "residual", BF16)
-    _launch("moe_combine", stream, (out, y, pos, weights, residual),
-            (_ptr(y), _ptr(pos), _ptr(weights), _ptr(residual), _ptr(out), t, k, rows, n))
+    _launch("moe_combine", stream, (y, pos, weights, residual, out), lambda p: (*p, t, k, rows, n))
 
 
 def _w4_shapes(x, w_packed, scale, zero):
     """(lead, n, k, group, scale type) of a 4-bit weight w_packed [*lead, N, K/2] for x [M, K]."""
     k = x.shape[1]
     lead, n = tuple(w_packed.shape[:-2]), w_packed.shape[-2]
-    _shape(x, tuple(x.shape[:1]) + (k,), "x_bf16", BF16)
+    _shape(x, (x.shape[0], k), "x_bf16", BF16)
     _shape(w_packed, lead + (n, k // 2), "w_packed", BYTES)
     cols = scale.shape[-1]
     if cols == 0 or k % cols:
         raise ValueError(f"scale: {cols} groups do not divide K = {k}")
     kind = _type(scale, "scale")
-    if tuple(scale.shape) != lead + (n, cols) or not scale.is_contiguous():
+    if scale.shape != lead + (n, cols) or not scale.is_contiguous():
         raise ValueError(f"scale: shape {tuple(scale.shape)}, expected contiguous {lead + (n, cols)}")
     if zero is not None:
         _shape(zero, lead + (n, cols), "zero", BYTES)
@@ -403,8 +416,8 @@ def w4a16_group_gemv(x_bf16, w_packed, scale, out, zero=None, stream=None):
         raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected two dimensions")
     m = x_bf16.shape[0]
     _shape(out, (m, n), "out", BF16)
-    _launch("w4a16_group_gemv", stream, (out, x_bf16, w_packed, scale, zero),
-            (_ptr(x_bf16), _ptr(w_packed), _ptr(scale), kind, _ptr(zero), group, _ptr(out), m, n, k))
+    _launch("w4a16_group_gemv", stream, (x_bf16, w_packed, scale, zero, out),
+            lambda p: (*p[:3], kind, p[3], group, p[4], m, n, k))
 
 
 def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, row_index=None, silu_mul=False,
@@ -416,6 +429,6 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
     if len(lead) != 1:
         raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected three dimensions")
     rows = _grouped_shapes(offsets, row_index, out, n // 2 if silu_mul else n, lead[0])
-    _launch("w4a16_group_gemv_experts", stream, (out, x_bf16, w_packed, scale, zero, offsets, row_index),
-            (_ptr(x_bf16), _ptr(w_packed), _ptr(scale), kind, _ptr(zero), group, _ptr(offsets), _ptr(row_index),
-             int(bool(silu_mul)), _ptr(out), x_bf16.shape[0], rows, lead[0], n, k))
+    _launch("w4a16_group_gemv_experts", stream, (x_bf16, w_packed, scale, zero, offsets, row_index, out),
+            lambda p: (*p[:3], kind, p[3], group, p[4], p[5], int(bool(silu_mul)), p[6], x_bf16.shape[0], rows,
+                       lead[0], n, k))

@@ -81,10 +81,7 @@ struct ClassedTiles {
 // while the work of every part of the list is spread over all XCDs (one run
 // per XCD, as the dense GEMM has it, gives some XCDs the full tiles and others
 // the experts' remainders).
-#ifndef RUN
-#define RUN 64
-#endif
-constexpr uint32_t kRun = RUN;
+constexpr uint32_t kRun = 32;
 __device__ __forceinline__ void grouped_tile_of(uint32_t wg, uint32_t tiles_m, uint32_t tiles_n, uint32_t &tm,
                                                 uint32_t &tn) {
     const uint32_t total = tiles_m * tiles_n, whole = total / (kXcds * kRun);
@@ -121,11 +118,7 @@ __global__ __launch_bounds__(256, 2) void grouped_kernel(
 #ifdef CONTIG
     tile_of<kGemmGroupM>(blockIdx.x, tiles_m, tiles_n, tm, tn);
 #else
-#ifdef CONTIG
-    tile_of<kGemmGroupM>(blockIdx.x, tiles_m, tiles_n, tm, tn);
-#else
     grouped_tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
-#endif
 #endif
     RowTile r = rt.find(tm);
     // the same in every lane; said so, since a buffer descriptor that the compiler
