@@ -34,8 +34,8 @@ int w4_check(const uint16_t *x, const uint8_t *w_packed, const void *scale, int 
     return BSR_OK;
 }
 
-bool w4_shape_ok(int scale_type, uint32_t group, uint32_t k) {
-    return k_ok(k) && type_ok(scale_type) &&
+bool w4_shape_ok(int scale_type, uint32_t group, uint32_t x_rows, uint32_t k) {
+    return k_ok(k) && k < bsr::kGemmTallMaxK && (uint64_t)x_rows * k < (1ull << 31) && type_ok(scale_type) &&
            (group == 0 || ((group == 32 || group == 64 || group == 128) && k % group == 0));
 }
 
@@ -107,7 +107,7 @@ int moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, con
 int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type,
                      const uint8_t *zero, uint32_t group, uint16_t *out, uint32_t m, uint32_t n, uint32_t k,
                      void *stream) {
-    if (!w4_shape_ok(scale_type, group, k) || m > kMaxRows) return BSR_EINVAL;
+    if (!w4_shape_ok(scale_type, group, m, k)) return BSR_EINVAL;
     if (m == 0 || n == 0) return BSR_OK;
     if (int st = w4_check(x, w_packed, scale, scale_type, out)) return st;
     if (div_up(m, 16) * div_up(n, 16) > kMaxGrid) return BSR_EINVAL;
@@ -120,7 +120,7 @@ int w4a16_group_gemv_experts(const uint16_t *x, const uint8_t *w_packed, const v
                              const uint8_t *zero, uint32_t group, const int32_t *offsets, const int32_t *row_index,
                              int silu_mul, uint16_t *out, uint32_t x_rows, uint32_t rows, uint32_t experts, uint32_t n,
                              uint32_t k, void *stream) {
-    if (!w4_shape_ok(scale_type, group, k) || !grouped_ok(row_index, x_rows, rows, experts)) return BSR_EINVAL;
+    if (!w4_shape_ok(scale_type, group, x_rows, k) || !grouped_ok(row_index, x_rows, rows, experts)) return BSR_EINVAL;
     if ((silu_mul != 0 && silu_mul != 1) || (silu_mul == 1 && n % 2 != 0)) return BSR_EINVAL;
     if (rows == 0 || n == 0 || experts == 0) return BSR_OK;
     if (!offsets) return BSR_ENULL;

@@ -41,52 +41,62 @@ inline uint64_t grouped_row_tiles(uint32_t rows, uint32_t experts, uint32_t bm) 
 }
 
 // ---- 4-bit group GEMV -------------------------------------------------------
-// A workgroup owns 16 output columns (with the SiLU product: of the gate and
-// of the up half) and up to 16 rows; its waves split K in chunks of 128, taken
-// kW4gPass at a time.  Up to kW4gFew rows the passes are twice as long.
+// A workgroup owns a tile of up to 16 rows, or 4, and 16 output columns, 32
+// (`ct` tiles of 16), or with the SiLU product 16 of the gate and 16 of the up
+// half; its waves split K in chunks of 128, several to a pass.
 constexpr uint32_t kW4gCols = 16;
 constexpr uint32_t kW4gRows = 16;
 constexpr uint32_t kW4gFew = 4;
 constexpr uint32_t kW4gChunk = 128;
-constexpr uint32_t kW4gMaxWaves = 16;
-#ifndef W4G_TARGET
-#define W4G_TARGET 6144
-#endif
-#ifndef W4G_CT2
-#define W4G_CT2 512
-#endif
 
-// Chunks per pass, and LDS bytes of one staged activation row (16 bytes of
-// padding spread the 16 rows read at one offset over the banks).
-BSR_HD constexpr uint32_t w4g_pass(bool few, uint32_t ct) { return few && ct == 1 ? 4 : 2; }
-BSR_HD constexpr uint32_t w4g_pitch(uint32_t pass) { return pass * kW4gChunk * 2 + 16; }
+// gpc: groups per chunk (0: one scale per weight row).
+// Chunks per pass: the weights in flight per wave, as many as the registers
+// hold beside the scales of a group of 32 and, from 5 rows on, the activations.
+BSR_HD constexpr uint32_t w4g_pass(uint32_t ct, uint32_t gpc) { return ct == 2 || gpc == 4 ? 2 : 4; }
+// Chunks per staging of the activations.
+BSR_HD constexpr uint32_t w4g_stage(uint32_t rows, uint32_t ct, uint32_t gpc) {
+    return rows <= kW4gFew ? w4g_pass(ct, gpc) : 2;
+}
+// LDS bytes of one staged row (16 of padding spread the 16 rows read at one
+// offset over the banks).
+BSR_HD constexpr uint32_t w4g_pitch(uint32_t stage) { return stage * kW4gChunk * 2 + 16; }
+// Waves per workgroup: 16 leave a wave 128 registers, which the kernels of one
+// column tile and few rows fit.
+BSR_HD constexpr uint32_t w4g_max_waves(uint32_t rows, uint32_t ct) { return rows <= kW4gFew && ct == 1 ? 16 : 8; }
 
 struct W4gPlan {
-    uint32_t ct;  // column tiles per workgroup (with the SiLU product: a gate and an up tile)
+    uint32_t rows;  // of a tile, at most: kW4gFew or kW4gRows
+    uint32_t ct;    // column tiles per workgroup (with the SiLU product: a gate and an up tile)
     uint32_t row_tiles, col_tiles, waves, chunks_per_wave, wave_bytes, lds;
 };
 
-// The rows of a tile are known only on the device: LDS and passes are sized
-// for the most there can be.
-inline W4gPlan w4_group_plan(uint32_t rows, uint32_t experts, uint32_t cols, uint32_t k, bool silu) {
+inline W4gPlan w4_group_plan(uint32_t rows, uint32_t experts, uint32_t cols, uint32_t k, uint32_t group, bool silu) {
     W4gPlan p;
-    const uint32_t most = rows < kW4gRows ? rows : kW4gRows;
+    const uint32_t gpc = group == 0 ? 0 : kW4gChunk / group;
+    const uint32_t used = rows < experts ? rows : experts;
+    // Tiles of 4 rows where an expert has 2 on average: a token's few rows, and
+    // less to stage; the experts with more read their weight again from cache
+    // (16 tokens over 64 experts with the SiLU product 66 us, with tiles of 16 68-71).
+    p.rows = rows <= kW4gFew || rows <= 2 * (uint64_t)used ? kW4gFew : kW4gRows;
     const uint32_t chunks = (uint32_t)div_up(k, kW4gChunk);
-    p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, kW4gRows);
-    p.ct = silu ? 2 : 1;
-    if (!silu && most > kW4gFew && p.row_tiles * div_up(cols, kW4gCols) >= W4G_CT2) p.ct = 2;
+    p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, p.rows);
+    // Two column tiles share the staged activations from 5 rows on, if that
+    // leaves every CU a workgroup (48 tokens, top 8 of 64 experts, N 4096, K 2048: 84 us
+    // against 98; at 256 tiles of 16 columns one tile each is faster, 15.5 against 20.5).
+    const uint64_t tiles = (uint64_t)p.row_tiles * div_up(cols, kW4gCols);
+    p.ct = silu || (p.rows > kW4gFew && tiles >= 2 * (uint64_t)kGemmCus) ? 2 : 1;
     p.col_tiles = (uint32_t)div_up(cols, kW4gCols * (silu ? 1 : p.ct));
-    uint64_t waves = div_up(W4G_TARGET, (uint64_t)p.row_tiles * p.col_tiles);
-    waves = waves < kW4gMaxWaves ? waves : kW4gMaxWaves;
+    // As many waves as run at once (16, 12 or 8 per CU by their registers), so
+    // that one round of workgroups takes the whole weight.
+    const uint32_t at_once = (p.rows > kW4gFew ? 8 : (p.ct == 2 ? 12 : 16)) * kGemmCus;
+    const uint32_t most = w4g_max_waves(p.rows, p.ct), pass = w4g_pass(p.ct, gpc);
+    uint64_t waves = at_once / ((uint64_t)p.row_tiles * p.col_tiles);
+    waves = waves > 1 ? waves : 1;
+    waves = waves < most ? waves : most;
     waves = waves < chunks ? waves : chunks;
-    const uint32_t pass = w4g_pass(most <= kW4gFew, p.ct);
-    uint32_t cpw = (uint32_t)div_up(chunks, waves);
-    if (cpw > pass) cpw = (uint32_t)div_up(cpw, pass) * pass;  // whole passes
-    p.chunks_per_wave = cpw;
-    p.waves = (uint32_t)div_up(chunks, cpw);
-    const uint32_t few = (most < kW4gFew ? most : kW4gFew) * w4g_pitch(w4g_pass(true, p.ct));
-    const uint32_t many = most <= kW4gFew ? 0 : kW4gRows * w4g_pitch(w4g_pass(false, p.ct));
-    p.wave_bytes = few > many ? few : many;
+    p.chunks_per_wave = (uint32_t)div_up(div_up(chunks, waves), pass) * pass;  // whole passes
+    p.waves = (uint32_t)div_up(chunks, p.chunks_per_wave);
+    p.wave_bytes = (rows < p.rows ? rows : p.rows) * w4g_pitch(w4g_stage(p.rows, p.ct, gpc));
     const uint32_t sums = p.waves * 64 * 4 * 4 * p.ct;
     p.lds = p.waves * p.wave_bytes;
     p.lds = p.lds > sums ? p.lds : sums;

@@ -26,11 +26,11 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// Eight codes -> BF16 16 + c, pairs (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w) {
-    constexpr uint32_t m = 0x00780078u, base = 0x41804180u;
-    const v4i v = {(int)((w << 3 & m) | base), (int)((w >> 1 & m) | base), (int)((w >> 5 & m) | base),
-                   (int)((w >> 9 & m) | base)};
+// Eight codes -> BF16 16 + c, pairs (0,4) (1,5) (2,6) (3,7); mask = 0x00780078.
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, uint32_t mask) {
+    constexpr uint32_t base = 0x41804180u;
+    const v4i v = {(int)((w << 3 & mask) | base), (int)((w >> 1 & mask) | base), (int)((w >> 5 & mask) | base),
+                   (int)((w >> 9 & mask) | base)};
     return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -52,25 +52,50 @@ __device__ __forceinline__ v4i swap_quarters(v4i w) {
     return v4i{(int)c[0], (int)d[0], (int)c[1], (int)d[1]};
 }
 
-// N consecutive elements of BYTES each, as one load wherever they start.
+// N consecutive elements of BYTES each, loaded as wide as they come wherever
+// they start (words and vectors of any alignment; held as words, since an
+// array filled byte-wise would live in memory).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
+
 template <int BYTES, int N>
 struct Run {
-    uint32_t raw[(BYTES * N + 3) / 4];
+    static constexpr int kBytes = BYTES * N, kWords = (kBytes + 3) / 4;
+    uint32_t raw[kWords];
 
-    __device__ __forceinline__ void load(const void *p, uint64_t at) {
-        __builtin_memcpy(raw, static_cast<const uint8_t *>(p) + at * BYTES, BYTES * N);
+    __device__ __forceinline__ void load(const uint8_t *from) {
+        if constexpr (kBytes == 1) raw[0] = *from;
+        if constexpr (kBytes == 2) raw[0] = *reinterpret_cast<const u16_any *>(from);
+        if constexpr (kBytes == 4) raw[0] = *reinterpret_cast<const u32_any *>(from);
+        if constexpr (kBytes == 8) {
+            const u32x2_any v = *reinterpret_cast<const u32x2_any *>(from);
+            raw[0] = v.x;
+            raw[1] = v.y;
+        }
+        if constexpr (kBytes >= 16) {
+            static_assert(kBytes % 16 == 0, "whole 16-byte words");
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const u32x4_any v = *reinterpret_cast<const u32x4_any *>(from + 4 * i);
+                raw[i] = v.x;
+                raw[i + 1] = v.y;
+                raw[i + 2] = v.z;
+                raw[i + 3] = v.w;
+            }
+        }
     }
-    // entries from `live` on repeat the last one
-    __device__ __forceinline__ void load_some(const void *p, uint64_t at, uint32_t live) {
-        const uint8_t *from = static_cast<const uint8_t *>(p) + at * BYTES;
+    // the first `live` entries; the others are 0
+    __device__ __forceinline__ void load_some(const uint8_t *from, uint32_t live) {
 #pragma unroll
         for (int i = 0; i < (BYTES * N + 3) / 4; ++i) raw[i] = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint8_t *e = from + (uint64_t)min((uint32_t)i, live - 1) * BYTES;
-            uint32_t v = e[0];
-            if constexpr (BYTES == 2) v = *reinterpret_cast<const uint16_t *>(e);
-            if constexpr (BYTES == 4) v = *reinterpret_cast<const uint32_t *>(e);
+            if ((uint32_t)i >= live) break;
+            uint32_t v = from[i * BYTES];
+            if constexpr (BYTES == 2) v = *reinterpret_cast<const u16_any *>(from + i * BYTES);
+            if constexpr (BYTES == 4) v = *reinterpret_cast<const u32_any *>(from + i * BYTES);
             raw[BYTES * i / 4] |= v << (8 * (BYTES * i % 4));
         }
     }
@@ -78,6 +103,9 @@ struct Run {
         return raw[BYTES * i / 4] >> (8 * (BYTES * i % 4)) & (BYTES == 4 ? ~0u : (1u << (8 * BYTES % 32)) - 1);
     }
 };
+
+template <int STYPE>
+constexpr uint32_t kScaleBytes = STYPE == 2 ? 4 : 2;
 
 template <int STYPE>
 __device__ __forceinline__ float scale_value(uint32_t bits) {
@@ -92,9 +120,16 @@ template <int GPC, int STYPE, int CT, int PC>
 struct Pass {
     static constexpr int kGroups = GPC > 0 ? GPC * PC : 1;
     v4i w[CT][PC];
-    Run<STYPE == 2 ? 4 : 2, kGroups> s[CT];
+    Run<kScaleBytes<STYPE>, kGroups> s[CT];
     Run<1, kGroups> z[CT];
 };
+
+constexpr int kRsrcWord3 = 0x00020000;         // raw buffer (gfx9)
+constexpr uint32_t kPastEnd = 0xFFFFFFE0u;     // an offset behind every buffer: reads as 0
+
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, uint32_t offset) {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0));
+}
 
 struct W4Args {
     const uint16_t *x;
@@ -110,64 +145,79 @@ struct W4Args {
 template <int GPC, int STYPE, int CT, bool SILU, int ROWS>
 __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, const RowTile &t, uint32_t col0,
                                         uint8_t *xs, int lane, int wave, v4f (&acc)[CT]) {
-    constexpr int PC = w4g_pass(ROWS <= (int)kW4gFew, CT);
-    constexpr uint32_t kPitch = w4g_pitch(PC);
-    constexpr int kLoads = ROWS * PC / 4;           // 16-byte activation loads per lane and pass
-    constexpr int kRowLoads = PC * kW4gChunk / 8;   // of which a row takes
+    constexpr int PC = w4g_pass(CT, GPC), XC = w4g_stage(ROWS, CT, GPC);  // chunks per pass, and per staging of x
+    constexpr uint32_t kPitch = w4g_pitch(XC);
+    constexpr int kLoads = ROWS * XC / 4;           // 16-byte activation loads per lane and staging
+    constexpr int kRowLoads = XC * kW4gChunk / 8;   // of which a row takes
+    static_assert(PC % XC == 0, "whole stagings per pass");
     const uint32_t c = lane & 15, q = lane >> 4;
     const uint32_t groups = GPC > 0 ? p.k / (kW4gChunk / GPC) : 1;
     const uint32_t chunks = (p.k + kW4gChunk - 1) / kW4gChunk;
     const uint32_t first = wave * p.chunks_per_wave, end = min(chunks, first + p.chunks_per_wave);
-    uint64_t wrow[CT];
+    // Addresses: a descriptor or base pointer that is the same in all lanes, a
+    // 32-bit offset per lane that stays, and the pass's offset as a scalar.
+    // Weight rows past the last column, and bytes past the buffer, read as 0.
+    __amdgpu_buffer_rsrc_t rw[CT];
+    const uint8_t *sbase[CT], *zbase[CT];
+    uint32_t srow[CT];  // scale row within the tile
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
-        wrow[ct] = (uint64_t)t.expert * p.n + (SILU ? ct * p.cols + min(col0 + c, p.cols - 1)
-                                                    : min(col0 + ct * kW4gCols + c, p.cols - 1));
+    for (int ct = 0; ct < CT; ++ct) {
+        const uint32_t c0 = SILU ? col0 : col0 + ct * kW4gCols;  // (CT 2: the second tile may lie past the end)
+        const uint32_t live = c0 < p.cols ? min(p.cols - c0, kW4gCols) : 0;
+        const uint64_t row = (uint64_t)t.expert * p.n + (SILU ? ct * p.cols : 0) + min(c0, p.cols - 1);
+        rw[ct] = __builtin_amdgcn_make_buffer_rsrc((void *)(p.w + row * (p.k / 2)), (short)0, (int)(live * (p.k / 2)),
+                                                   kRsrcWord3);
+        sbase[ct] = static_cast<const uint8_t *>(p.scale) + row * groups * kScaleBytes<STYPE>;
+        zbase[ct] = p.zero + row * groups;
+        srow[ct] = live == 0 ? 0 : min(c, live - 1);
+    }
+    const uint32_t wo = c * (p.k / 2) + 16 * q;
 
     // activation loads: load i brings 16 bytes of row (64 * i + lane) / kRowLoads
-    int32_t xsrc[kLoads];
+    const __amdgpu_buffer_rsrc_t rx =
+        __builtin_amdgcn_make_buffer_rsrc((void *)p.x, (short)0, (int)(g.src_rows * p.k * 2), kRsrcWord3);
+    uint32_t xo[kLoads];
+    const uint32_t xk = lane % kRowLoads * 8;  // its element within the staging
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
         const uint32_t row = (64 * i + lane) / kRowLoads;
-        xsrc[i] = row < t.rows ? source_row(g, t.row0 + row) : -1;
+        const int32_t src = row < t.rows ? source_row(g, t.row0 + row) : -1;
+        xo[i] = src >= 0 ? ((uint32_t)src * p.k + xk) * 2 : kPastEnd;
     }
-    const uint32_t xk = lane % kRowLoads * 8;  // its element within the pass
 
+    // A pass comes in whole (all its chunks in this wave's range and inside K)
+    // or, as the wave's last one, in part: then chunks past the range are
+    // skipped, and past K the activations are 0 and codes and scales any.
     using P = Pass<GPC, STYPE, CT, PC>;
     v4i xv[kLoads];
-    auto load = [&](P &b, uint32_t chunk) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < PC; ++i) {
-            if (chunk + i >= end) break;
-            const uint32_t k0 = (chunk + i) * kW4gChunk;
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const uint32_t byte = min(k0 / 2 + 16 * q, p.k / 2 - 16);  // past K: any codes, the activations are 0
-                b.w[ct][i] = *reinterpret_cast<const v4i *>(p.w + wrow[ct] * (p.k / 2) + byte);
-            }
-        }
+    auto load = [&](P &b, uint32_t chunk, bool part) __attribute__((always_inline)) {
         if constexpr (GPC > 0) {
             const uint32_t g0 = chunk * GPC;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                const uint64_t at = wrow[ct] * groups + g0;
-                if (g0 + GPC * PC <= groups) {
-                    b.s[ct].load(p.scale, at);
-                    if (p.zero != nullptr) b.z[ct].load(p.zero, at);
-                } else {  // the row's last pass (past K the activations are 0)
-                    b.s[ct].load_some(p.scale, at, groups - g0);
-                    if (p.zero != nullptr) b.z[ct].load_some(p.zero, at, groups - g0);
+                const uint8_t *sp = sbase[ct] + g0 * kScaleBytes<STYPE> + srow[ct] * (groups * kScaleBytes<STYPE>);
+                const uint8_t *zp = zbase[ct] + g0 + srow[ct] * groups;
+                if (!part || g0 + GPC * PC <= groups) {
+                    b.s[ct].load(sp);
+                    if (p.zero != nullptr) b.z[ct].load(zp);
+                } else {
+                    b.s[ct].load_some(sp, groups - g0);
+                    if (p.zero != nullptr) b.z[ct].load_some(zp, groups - g0);
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < PC; ++i)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+                b.w[ct][i] = load16(rw[ct], wo, (chunk + i) * (kW4gChunk / 2));
     };
-    auto load_x = [&](uint32_t chunk) __attribute__((always_inline)) {
-        const uint32_t k0 = chunk * kW4gChunk + xk, kend = min(p.k, end * kW4gChunk);
+    auto load_x = [&](uint32_t chunk, bool part) __attribute__((always_inline)) {
+        const bool live = !part || chunk * kW4gChunk + xk < p.k;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            xv[i] = v4i{0, 0, 0, 0};
-            if (xsrc[i] >= 0 && k0 < kend)
-                xv[i] = *reinterpret_cast<const v4i *>(p.x + (uint64_t)(uint32_t)xsrc[i] * p.k + k0);
+            if (ROWS <= (int)kW4gFew && 64u * i / kRowLoads >= t.rows) break;
+            xv[i] = load16(rx, live ? xo[i] : kPastEnd, chunk * (kW4gChunk * 2));
         }
     };
     auto store_x = [&]() __attribute__((always_inline)) {
@@ -181,27 +231,32 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
     const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
     const v4i one4 = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
     const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+    uint32_t mask = 0x00780078u;  // in a register of its own: v_and_or_b32 takes one constant
+    asm("" : "+v"(mask));
     v4f psum[CT], xsum = none;  // GPC 0: over the wave's whole range
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) acc[ct] = psum[ct] = none;
     const uint8_t *xa = xs + min(c, t.rows - 1) * kPitch + 16 * q;
-    auto compute = [&](const P &b, uint32_t chunk) __attribute__((always_inline)) {
+    // chunks [i0, i0 + XC) of a pass, whose activations are staged
+    auto compute = [&](const P &b, int i0, uint32_t live) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < PC; ++i) {
-            if (chunk + i >= end) break;
+        for (int ii = 0; ii < XC; ++ii) {
+            const int i = i0 + ii;
+            if ((uint32_t)i >= live) break;
+            asm volatile("" ::: "memory");  // a chunk's reads stay with it: bounds live registers
             v4i w[CT];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) w[ct] = swap_quarters(b.w[ct][i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bf16x8 xv8 = *reinterpret_cast<const bf16x8 *>(xa + i * (kW4gChunk * 2) + j * 64);
+                const bf16x8 xv8 = *reinterpret_cast<const bf16x8 *>(xa + ii * (kW4gChunk * 2) + j * 64);
                 constexpr int per = GPC > 0 ? 4 / GPC : 4;
                 if (GPC > 0 && j % per == 0) xsum = none;
                 xsum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv8, ones, xsum, 0, 0, 0);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     if (GPC > 0 && j % per == 0) psum[ct] = none;
-                    psum[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv8, codes_to_bf16((uint32_t)w[ct][j]),
+                    psum[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv8, codes_to_bf16((uint32_t)w[ct][j], mask),
                                                                        psum[ct], 0, 0, 0);
                     if (GPC > 0 && j % per == per - 1) {
                         const float s = scale_value<STYPE>(b.s[ct].bits(i * GPC + j / per));
@@ -214,45 +269,78 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
             }
         }
     };
-
-    if (first < end) {
-        P b[2];
-        load_x(first);
-        load(b[0], first);
-        for (uint32_t at = first; at < end; at += 2 * PC) {
+    // One whole pass; `more`: the next one is whole too, and its loads go out
+    // before this one is computed.  Loads return in order, so a staging's
+    // activations are asked for before the next pass's weights wherever they
+    // are needed before them.  (more is a constant at each call: a load that
+    // may or may not have been issued would make every later wait the longer one.)
+    auto pass = [&](P &b, P &next, uint32_t chunk, bool more) __attribute__((always_inline)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint32_t chunk = at + u * PC;
-                if (chunk >= end) break;
-                store_x();
-                if (chunk + PC < end) {
-                    load_x(chunk + PC);
-                    load(b[1 - u], chunk + PC);
-                }
-                compute(b[u], chunk);
+        for (int i = 0; i < PC; i += XC) {
+            store_x();
+            if (i + XC < PC)
+                load_x(chunk + i + XC, false);
+            else if (more)
+                load_x(chunk + PC, false);
+            if (i == 0 && more) load(next, chunk + PC, false);
+            compute(b, i, PC);
+        }
+    };
+    const uint32_t whole = min(end, p.k / kW4gChunk);           // chunks before this one are whole
+    const uint32_t passes = first < whole ? (whole - first) / PC : 0;
+    P b0, b1;
+    uint32_t chunk = first;
+    if (passes > 0) {
+        load_x(chunk, false);
+        load(b0, chunk, false);
+        const uint32_t last = first + (passes - 1) * PC;
+        for (;;) {
+            if (chunk == last) {
+                pass(b0, b1, chunk, false);
+                break;
             }
+            pass(b0, b1, chunk, true);
+            chunk += PC;
+            if (chunk == last) {
+                pass(b1, b0, chunk, false);
+                break;
+            }
+            pass(b1, b0, chunk, true);
+            chunk += PC;
+        }
+        chunk += PC;
+    }
+    if (chunk < end) {
+        load_x(chunk, true);
+        load(b0, chunk, true);
+#pragma unroll
+        for (int i = 0; i < PC; i += XC) {
+            if (chunk + i >= end) break;
+            if (i > 0) load_x(chunk + i, true);
+            store_x();
+            compute(b0, i, end - chunk);
         }
     }
     if constexpr (GPC == 0) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            const float s = load_f32<STYPE>(p.scale, wrow[ct]);
-            const float z = p.zero != nullptr ? (float)p.zero[wrow[ct]] : 8.0f;
+            const float s = load_f32<STYPE>(sbase[ct], srow[ct]);
+            const float z = p.zero != nullptr ? (float)zbase[ct][srow[ct]] : 8.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[ct][r] = s * fmaf(-16.0f - z, xsum[r], psum[ct][r]);
         }
     }
 }
 
-template <int GPC, int STYPE, int CT, bool SILU>
-__global__ __launch_bounds__(kW4gMaxWaves * 64) void w4_group_kernel(W4Args p, GroupedRows g, uint32_t col_tiles,
-                                                                     uint32_t wave_bytes) {
+template <int GPC, int STYPE, int CT, bool SILU, int ROWS>
+__global__ __launch_bounds__(w4g_max_waves(ROWS, CT) * 64) void w4_group_kernel(W4Args p, GroupedRows g,
+                                                                            uint32_t col_tiles, uint32_t wave_bytes) {
     static_assert(!SILU || CT == 2, "a gate and an up tile");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nwaves = blockDim.x >> 6;
-    RowTile t = RowTiles(g, kW4gRows, lane).find(blockIdx.x / col_tiles);
+    RowTile t = RowTiles(g, ROWS, lane).find(blockIdx.x / col_tiles);
     t.expert = __builtin_amdgcn_readfirstlane(t.expert);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     t.rows = __builtin_amdgcn_readfirstlane(t.rows);
@@ -260,11 +348,7 @@ __global__ __launch_bounds__(kW4gMaxWaves * 64) void w4_group_kernel(W4Args p, G
     constexpr uint32_t kOut = SILU ? 1 : CT;  // output column tiles
     const uint32_t col0 = blockIdx.x % col_tiles * (kOut * kW4gCols);
     v4f acc[CT];
-    uint8_t *xs = smem + wave * wave_bytes;
-    if (t.rows <= kW4gFew)
-        w4_rows<GPC, STYPE, CT, SILU, kW4gFew>(p, g, t, col0, xs, lane, wave, acc);
-    else
-        w4_rows<GPC, STYPE, CT, SILU, kW4gRows>(p, g, t, col0, xs, lane, wave, acc);
+    w4_rows<GPC, STYPE, CT, SILU, ROWS>(p, g, t, col0, smem + wave * wave_bytes, lane, wave, acc);
 
     // the waves' sums, added in wave order
     __syncthreads();
@@ -289,15 +373,26 @@ __global__ __launch_bounds__(kW4gMaxWaves * 64) void w4_group_kernel(W4Args p, G
     }
 }
 
-template <int STYPE, int CT, bool SILU>
+template <int STYPE, int CT, bool SILU, int ROWS>
 hipError_t launch(const W4Args &p, const GroupedRows &g, uint32_t group, const W4gPlan &plan, hipStream_t s) {
-    auto kernel = group == 32    ? w4_group_kernel<4, STYPE, CT, SILU>
-                  : group == 64  ? w4_group_kernel<2, STYPE, CT, SILU>
-                  : group == 128 ? w4_group_kernel<1, STYPE, CT, SILU>
-                                 : w4_group_kernel<0, STYPE, CT, SILU>;
+    auto kernel = group == 32    ? w4_group_kernel<4, STYPE, CT, SILU, ROWS>
+                  : group == 64  ? w4_group_kernel<2, STYPE, CT, SILU, ROWS>
+                  : group == 128 ? w4_group_kernel<1, STYPE, CT, SILU, ROWS>
+                                 : w4_group_kernel<0, STYPE, CT, SILU, ROWS>;
     hipLaunchKernelGGL(kernel, dim3(plan.col_tiles * plan.row_tiles), dim3(64 * plan.waves), plan.lds, s, p, g,
                        plan.col_tiles, plan.wave_bytes);
     return hipGetLastError();
+}
+
+template <int STYPE>
+hipError_t launch_rows(const W4Args &p, const GroupedRows &g, uint32_t group, bool silu, const W4gPlan &plan,
+                       hipStream_t s) {
+    if (plan.rows == kW4gFew)
+        return silu ? launch<STYPE, 2, true, kW4gFew>(p, g, group, plan, s)
+                    : launch<STYPE, 1, false, kW4gFew>(p, g, group, plan, s);
+    if (silu) return launch<STYPE, 2, true, kW4gRows>(p, g, group, plan, s);
+    return plan.ct == 2 ? launch<STYPE, 2, false, kW4gRows>(p, g, group, plan, s)
+                        : launch<STYPE, 1, false, kW4gRows>(p, g, group, plan, s);
 }
 
 }  // namespace
@@ -306,17 +401,12 @@ hipError_t launch_w4_group(const uint16_t *x, const uint8_t *w, const void *scal
                            const uint8_t *zero, uint32_t group, uint16_t *out, const GroupedRows &g, bool silu,
                            uint32_t n, uint32_t k, hipStream_t s) {
     const uint32_t cols = silu ? n / 2 : n;
-    const W4gPlan plan = w4_group_plan(g.rows, g.experts, cols, k, silu);
+    const W4gPlan plan = w4_group_plan(g.rows, g.experts, cols, k, group, silu);
     if (plan.lds > kLdsBytes) return hipErrorInvalidValue;
     const W4Args p = {x, w, scale, zero, out, n, k, cols, plan.chunks_per_wave};
-#define BSR_W4G(T)                                                 \
-    silu           ? launch<T, 2, true>(p, g, group, plan, s)      \
-    : plan.ct == 2 ? launch<T, 2, false>(p, g, group, plan, s)     \
-                   : launch<T, 1, false>(p, g, group, plan, s)
-    if (scale_type == 0) return BSR_W4G(0);
-    if (scale_type == 1) return BSR_W4G(1);
-    return BSR_W4G(2);
-#undef BSR_W4G
+    if (scale_type == 0) return launch_rows<0>(p, g, group, silu, plan, s);
+    if (scale_type == 1) return launch_rows<1>(p, g, group, silu, plan, s);
+    return launch_rows<2>(p, g, group, silu, plan, s);
 }
 
 }  // namespace bsr

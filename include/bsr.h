@@ -413,7 +413,9 @@ BSR_API int moe_combine(const uint16_t *y, const int32_t *pos, const float *weig
  * and (16 + z) * sum(x) is taken off, then the scale is applied once, so the
  * error of a sum is bounded with the terms |x| * scale * (32 + c + z).
  * Meant for m <= 16; every further 16 rows read the weight once more.
- * Errors: BSR_EINVAL (k, group, scale_type, more than 2^31 workgroups),
+ * Limits: k < 2^24, m * k < 2^31 (the activations are read with 32-bit offsets).
+ * Errors: BSR_EINVAL (k, group, scale_type, those limits, more than 2^31
+ * workgroups),
  * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
  */
 BSR_API int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type,
@@ -429,7 +431,7 @@ BSR_API int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const v
  *            and n/2..n-1 the up projection, out [rows, n/2] =
  *            bf16_rne( fl32(gate / fl32(1 + exp(-gate))) * up ), gate and up in
  *            binary32; n must be even
- * Limits: experts <= 65536, rows < 2^31.
+ * Limits: experts <= 65536, rows < 2^31, k < 2^24, x_rows * k < 2^31.
  * Errors: as w4a16_group_gemv; BSR_EINVAL too for x_rows < rows without
  * row_index, silu_mul other than 0 or 1, an odd n with it, and those limits.
  */

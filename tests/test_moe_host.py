@@ -74,14 +74,14 @@ def test_combine_refusals(change, status):
 
 W4_BOTH = [
     (dict(k=0), INV), (dict(k=48), INV), (dict(group=16), INV), (dict(group=64, k=96), INV), (dict(group=256), INV),
-    (dict(scale_type=3), INV), (dict(scale_type=-1), INV), (dict(n=0), OK), (dict(x=None), NUL), (dict(w=None), NUL),
+    (dict(k=1 << 24), INV), (dict(scale_type=3), INV), (dict(scale_type=-1), INV), (dict(n=0), OK), (dict(x=None), NUL), (dict(w=None), NUL),
     (dict(scale=None), NUL), (dict(out=None), NUL), (dict(x=_fake(8)), ALI), (dict(w=_fake(8)), ALI),
     (dict(scale=_fake(1)), ALI), (dict(scale=_fake(2), scale_type=2), ALI), (dict(out=_fake(1)), ALI),
 ]
 
 
-@pytest.mark.parametrize("change, status", W4_BOTH + [(dict(m=0), OK), (dict(m=1 << 31), INV),
-                                                      (dict(m=1 << 30, n=1 << 12), INV)])
+@pytest.mark.parametrize("change, status", W4_BOTH + [(dict(m=0), OK), (dict(m=1 << 31), INV), (dict(m=1 << 25), INV),
+                                                      (dict(m=1 << 24, n=1 << 16), INV)])
 def test_w4_group_refusals(change, status):
     assert _call("w4a16_group_gemv", W4, **change) == status
 
@@ -89,7 +89,7 @@ def test_w4_group_refusals(change, status):
 @pytest.mark.parametrize("change, status", W4_BOTH + [
     (dict(rows=0), OK), (dict(experts=0), OK), (dict(rows=5), INV), (dict(experts=65537), INV), (dict(silu_mul=2), INV),
     (dict(silu_mul=1, n=7), INV), (dict(offsets=None), NUL), (dict(offsets=_fake(2)), ALI),
-    (dict(row_index=_fake(2)), ALI), (dict(rows=1 << 31), INV),
+    (dict(row_index=_fake(2)), ALI), (dict(rows=1 << 31), INV), (dict(x_rows=1 << 25), INV),
 ])
 def test_w4_experts_refusals(change, status):
     assert _call("w4a16_group_gemv_experts", W4E, **change) == status
