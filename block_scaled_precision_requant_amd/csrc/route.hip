@@ -1,11 +1,12 @@
 // route.hip -- the expert router and the weighted sum back to the tokens.
 //
 // Router.  For each token the top_k experts by logit, their weights, and the
-// stable order of all (token, slot) pairs by expert.  One wave per row: a lane
-// holds VPL consecutive logits as order-preserving 32-bit keys, and each of the
-// top_k steps is one wave maximum; the lowest lane (hence the lowest index)
-// that holds it wins.  Key 0 marks what is never taken (-inf, NaN, behind the
-// row's end).  The order is a counting sort without global atomics: every
+// stable order of all (token, slot) pairs by expert.  A row takes 16, 32 or 64
+// lanes (up to four rows per wave): a lane holds VPL consecutive logits as
+// order-preserving 32-bit keys, sorted once, and each of the top_k steps is one
+// maximum over the lanes' first keys; the lowest lane (hence the lowest index)
+// that holds it wins and moves on to its next.  Key 0 marks what is never taken
+// (-inf, NaN, behind the row's end).  The order is a counting sort without global atomics: every
 // block of tokens counts its experts (workspace, [block][expert]), a second
 // launch sums the counts of the blocks before it and ranks its own slots 1024
 // at a time -- within a wave by ballots over the bits of the expert id, across
@@ -28,81 +29,154 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor(v, d));
+// Reductions over segments of L = 16, 32 or 64 lanes, the result in every lane:
+// rotations within the rows of 16, then swaps of rows.
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int L, class F>
+__device__ __forceinline__ uint32_t segment_reduce(uint32_t v, F f) {
+    v = f(v, row_ror<8>(v));
+    v = f(v, row_ror<4>(v));
+    v = f(v, row_ror<2>(v));
+    v = f(v, row_ror<1>(v));
+    if constexpr (L >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = f(p[0], p[1]);
+    }
+    if constexpr (L >= 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = f(p[0], p[1]);
+    }
     return v;
 }
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+template <int L>
+__device__ __forceinline__ uint32_t segment_max(uint32_t v) {
+    return segment_reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int L>
+__device__ __forceinline__ float segment_sum(float v) {
+    return __uint_as_float(segment_reduce<L>(
+        __float_as_uint(v), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
 }
 
-// Top-k of one row by one wave; lane j < top_k ends with slot j's id (-1:
-// none) and weight.
+// VPL consecutive logits from element e of a row of `experts` (aligned to the
+// element only); those past the end read as -inf.
 template <int TYPE, int VPL>
-__device__ __forceinline__ void select_row(const void *logits, uint64_t row_at, uint32_t experts, uint32_t top_k,
-                                           bool sigmoid, bool renorm, float scale, int lane, int32_t &id,
-                                           float &weight) {
-    uint32_t key[VPL];
-    const uint32_t e0 = lane * VPL;
+__device__ __forceinline__ void load_logits(const void *logits, uint64_t row_at, uint32_t e, uint32_t experts,
+                                            float (&v)[VPL]) {
+    if constexpr (TYPE == 2) {
+        typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+        if (e + VPL <= experts) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = e0 + j < experts ? logit_key(load_f32<TYPE>(logits, row_at + e0 + j)) : 0;
-    uint32_t all[VPL];
+            for (int j = 0; j < VPL; j += 4) {
+                const f4 x = *reinterpret_cast<const f4 *>(static_cast<const float *>(logits) + row_at + e + j);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) all[j] = key[j];
-
-    id = -1;
-    uint32_t taken = 0, top = 0;  // lane j: key of slot j; the row's largest key
-    for (uint32_t s = 0; s < top_k; ++s) {
-        uint32_t best = key[0];
-        int at = 0;
-#pragma unroll
-        for (int j = 1; j < VPL; ++j)
-            if (key[j] > best) {
-                best = key[j];
-                at = j;
+                for (int i = 0; i < 4; ++i) v[j + i] = x[i];
             }
-        const uint32_t m = wave_max(best);
-        if (m == 0) break;
-        const int owner = __builtin_ctzll(__ballot(best == m));
-        const int oat = __builtin_amdgcn_readlane(at, owner);
+            return;
+        }
+    } else {
+        typedef uint16_t h4 __attribute__((ext_vector_type(4), aligned(2)));
+        if (e + VPL <= experts) {
 #pragma unroll
-        for (int j = 0; j < VPL; ++j)
-            if (lane == owner && j == oat) key[j] = 0;
-        if (s == 0) top = m;
-        if ((uint32_t)lane == s) {
-            id = owner * VPL + oat;
-            taken = m;
+            for (int j = 0; j < VPL; j += 4) {
+                const h4 x = *reinterpret_cast<const h4 *>(static_cast<const uint16_t *>(logits) + row_at + e + j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[j + i] = TYPE == 0 ? bf16_to_f32(x[i]) : (float)__builtin_bit_cast(_Float16, (uint16_t)x[i]);
+            }
+            return;
         }
     }
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+        v[j] = e + j < experts ? load_f32<TYPE>(logits, row_at + e + j) : -__builtin_huge_valf();
+}
+
+// Top-k of one row by a segment of L lanes, VPL consecutive experts each (v: this
+// lane's logits).  One lane hands slot s's id to found(s, id); lane j < top_k of
+// the segment returns slot j's weight, and whether there is one.
+template <int VPL, int L, class F>
+__device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k, bool sigmoid, bool renorm, float scale, int lane, F found,
+                                           float &weight) {
+    const uint32_t sl = lane % L;  // lane within the segment
+    uint32_t key[VPL], all[VPL];
+    uint32_t id[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+        key[j] = all[j] = logit_key(v[j]);
+        id[j] = sl * VPL + j;
+    }
+    // this lane's experts in falling order, equal ones by index
+#pragma unroll
+    for (int n = VPL - 1; n > 0; --n)
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            // (masks, not selects: a select between two elements would make the index dynamic)
+            const uint32_t a = key[j], b = key[j + 1];
+            const uint32_t d = (id[j] ^ id[j + 1]) & (b > a ? ~0u : 0u);
+            key[j] = max(a, b);
+            key[j + 1] = min(a, b);
+            id[j] ^= d;
+            id[j + 1] ^= d;
+        }
+    uint32_t taken = 0, top = 0, slot_id = 0;  // lane j: key and id of slot j; the row's largest key
+    for (uint32_t s = 0; s < top_k; ++s) {
+        const uint32_t m = segment_max<L>(key[0]);
+        const uint64_t have = __ballot(m != 0 && key[0] == m);
+        if (have == 0) break;  // no segment has an expert left
+        bool won;
+        if constexpr (L == 64)
+            won = lane == __builtin_ctzll(have);
+        else
+            won = (have >> (lane & ~(L - 1)) & ((1ull << L) - 1) & ((2ull << sl) - 1)) == 1ull << sl;
+        if (s == 0) top = m;
+        if (sl == s) taken = m;
+        if constexpr (L == 64) {  // one owner per wave: its id comes as a scalar, stored with all the others at the end
+            const uint32_t oid = __builtin_amdgcn_readlane(id[0], __builtin_ctzll(have));
+            if (sl == s) slot_id = oid;
+        } else if (won) {
+            found(s, id[0]);
+        }
+        if (won) {
+#pragma unroll
+            for (int j = 0; j + 1 < VPL; ++j) {
+                key[j] = key[j + 1];
+                id[j] = id[j + 1];
+            }
+            key[VPL - 1] = 0;
+        }
+    }
+    if (L == 64 && taken != 0) found(sl, slot_id);
     const float vmax = top != 0 ? key_logit(top) : 0.0f;
     // exp(v - vmax) with equal infinities at distance 0
     auto rel = [&](uint32_t k) {
-        const float v = key_logit(k);
-        return k == 0 ? 0.0f : expf(v == vmax ? 0.0f : v - vmax);
+        const float x = key_logit(k);
+        return k == 0 ? 0.0f : expf(x == vmax ? 0.0f : x - vmax);
     };
     float p;
     if (sigmoid) {
         // 1 / (1 + e^-v) and e^(v - m) / (1 + e^v); a renormalised row of large
         // negative logits keeps its ratios through the common factor e^-m
-        const float v = key_logit(taken);
+        const float x = key_logit(taken);
         const float m = renorm ? fminf(vmax, 0.0f) : 0.0f;
-        p = taken == 0 ? 0.0f : (v >= 0.0f ? 1.0f / (1.0f + expf(-v)) : expf(v - m) / (1.0f + expf(v)));
+        p = taken == 0 ? 0.0f : (x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - m) / (1.0f + expf(x)));
     } else {
         p = rel(taken);
     }
     float total = 1.0f;
     if (renorm) {
-        total = wave_sum(p);
+        total = segment_sum<L>(p);
     } else if (!sigmoid) {
         float part = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) part += rel(all[j]);
-        total = wave_sum(part);
+        total = segment_sum<L>(part);
     }
     weight = taken == 0 ? 0.0f : p / total * scale;
+    return taken != 0;
 }
 
 struct RouteShared {
@@ -174,7 +248,7 @@ __device__ __forceinline__ void place_slots(RouteShared &sh, const int32_t *ids,
     }
 }
 
-template <int TYPE, int VPL>
+template <int TYPE, int VPL, int L>
 __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(
     const void *__restrict__ logits, uint32_t ld, int32_t *ids, float *__restrict__ weights,
     int32_t *__restrict__ offsets, int32_t *__restrict__ row_token, int32_t *__restrict__ pos, uint32_t tokens,
@@ -188,14 +262,31 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(
         sh.before[tid] = 0;
     }
     __syncthreads();
-    for (uint32_t t = t0 + wave; t < t1; t += kRouteWaves) {
-        int32_t id;
+    // a row's logits are asked for while the row before it is worked on
+    constexpr uint32_t kRowsPerWave = 64 / L, kStep = kRouteWaves * kRowsPerWave;
+    const uint32_t e0 = lane % L * VPL;
+    uint32_t t = t0 + wave * kRowsPerWave + lane / L;
+    float next[VPL];
+    load_logits<TYPE, VPL>(logits, (uint64_t)t * ld, t < t1 ? e0 : experts, experts, next);
+    for (uint32_t tw = t0 + wave * kRowsPerWave; tw < t1; tw += kStep, t += kStep) {
+        float v[VPL];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) v[j] = next[j];
+        load_logits<TYPE, VPL>(logits, (uint64_t)(t + kStep) * ld, t + kStep < t1 ? e0 : experts, experts, next);
+        const bool live = t < t1;
+        const uint64_t out = (uint64_t)t * top_k;
         float w;
-        select_row<TYPE, VPL>(logits, (uint64_t)t * ld, experts, top_k, sigmoid, renorm, scale, lane, id, w);
-        if ((uint32_t)lane < top_k) {
-            ids[(uint64_t)t * top_k + lane] = id;
-            weights[(uint64_t)t * top_k + lane] = w;
-            if (id >= 0) atomicAdd(&sh.total[id], 1u);  // LDS integer counts: any order gives the same
+        const bool any = select_row<VPL, L>(
+            v, top_k, sigmoid, renorm, scale, lane,
+            [&](uint32_t s, uint32_t id) {
+                ids[out + s] = (int32_t)id;
+                atomicAdd(&sh.total[id], 1u);  // LDS integer counts: any order gives the same
+            },
+            w);
+        const uint32_t sl = lane % L;
+        if (live && sl < top_k) {
+            weights[out + sl] = w;
+            if (!any) ids[out + sl] = -1;
         }
     }
     __syncthreads();
@@ -230,10 +321,18 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
     const uint32_t e = tid % cols, part = tid / cols, parts = kRouteThreads / cols;
     if (e < experts) {
         uint32_t sum = 0, mine = 0;
-        for (uint32_t b = part; b < gridDim.x; b += parts) {
-            const uint32_t c = hist[(uint64_t)b * experts + e];
-            sum += c;
-            if (b < blockIdx.x) mine += c;
+        for (uint32_t b0 = part; b0 < gridDim.x; b0 += 16 * parts) {
+            uint32_t c[16];  // 16 loads at a time
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t b = b0 + i * parts;
+                c[i] = b < gridDim.x ? hist[(uint64_t)b * experts + e] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sum += c[i];
+                mine += b0 + i * parts < blockIdx.x ? c[i] : 0;
+            }
         }
         atomicAdd(&sh.total[e], sum);
         atomicAdd(&sh.before[e], mine);
@@ -255,20 +354,20 @@ void launch_select(const void *logits, uint32_t ld, int32_t *ids, float *weights
                    int32_t *pos, uint32_t tokens, uint32_t experts, uint32_t top_k, bool sigmoid, bool renorm,
                    float scale, uint32_t *hist, const RoutePlan &plan, hipStream_t s) {
     const uint32_t grid = plan.blocks == 0 ? 1 : plan.blocks;
-#define BSR_ROUTE(V)                                                                                             \
-    hipLaunchKernelGGL((route_select_kernel<TYPE, V>), dim3(grid), dim3(kRouteThreads), 0, s, logits, ld, ids,    \
+#define BSR_ROUTE(V, L)                                                                                          \
+    hipLaunchKernelGGL((route_select_kernel<TYPE, V, L>), dim3(grid), dim3(kRouteThreads), 0, s, logits, ld, ids,    \
                        weights, offsets, row_token, pos, tokens, experts, top_k, sigmoid, renorm, scale, hist,    \
                        plan.per_block)
     if (experts <= 64)
-        BSR_ROUTE(1);
+        BSR_ROUTE(4, 16);
     else if (experts <= 128)
-        BSR_ROUTE(2);
+        BSR_ROUTE(4, 32);
     else if (experts <= 256)
-        BSR_ROUTE(4);
+        BSR_ROUTE(4, 64);
     else if (experts <= 512)
-        BSR_ROUTE(8);
+        BSR_ROUTE(8, 64);
     else
-        BSR_ROUTE(16);
+        BSR_ROUTE(16, 64);
 #undef BSR_ROUTE
 }
 
