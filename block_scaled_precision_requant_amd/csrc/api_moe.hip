@@ -45,6 +45,7 @@ extern "C" {
 
 uint64_t moe_route_ws_bytes(uint32_t tokens, uint32_t experts, uint32_t top_k) {
     (void)top_k;
+    if (experts == 0 || experts > bsr::kRouteMaxExperts) return 0;  // moe_route refuses these
     return bsr::moe_route_plan(tokens, experts).bytes;
 }
 
@@ -64,7 +65,7 @@ int moe_route(const void *logits, int type, uint32_t ld, int32_t *ids, float *we
     const bsr::RoutePlan plan = bsr::moe_route_plan(tokens, experts);
     if (plan.bytes != 0) {
         if (!workspace) return BSR_ENULL;
-        if (!aligned(workspace, 4)) return BSR_EALIGN;
+        if (!aligned(workspace, 16)) return BSR_EALIGN;
         if (workspace_bytes < plan.bytes) return BSR_EINVAL;
     }
     if (int st = check_device()) return st;

@@ -17,18 +17,21 @@ constexpr uint32_t kRouteWaves = kRouteThreads / 64;
 constexpr uint32_t kRouteMaxBlocks = 256;
 
 // Tokens are cut into `blocks` runs of `per_block`; each run's expert counts
-// go to the workspace ([block][expert] u32).  One block needs no workspace.
+// go to the workspace ([block][pitch] u32, a pitch of whole 16 bytes; in all at
+// most 1024 bytes per expert).  One block needs no workspace.
 struct RoutePlan {
     uint32_t blocks, per_block;
     uint64_t bytes;
 };
+BSR_HD constexpr uint32_t route_pitch(uint32_t experts) { return (experts + 3) & ~3u; }
 
 inline RoutePlan moe_route_plan(uint32_t tokens, uint32_t experts) {
     RoutePlan p;
-    p.per_block = (uint32_t)div_up(tokens, kRouteMaxBlocks);
+    const uint32_t most = kRouteMaxBlocks * experts / route_pitch(experts);
+    p.per_block = (uint32_t)div_up(tokens, most);
     p.per_block = p.per_block < 2 * kRouteWaves ? 2 * kRouteWaves : p.per_block;
     p.blocks = (uint32_t)div_up(tokens, p.per_block);
-    p.bytes = p.blocks <= 1 ? 0 : (uint64_t)p.blocks * experts * 4;
+    p.bytes = p.blocks <= 1 ? 0 : (uint64_t)p.blocks * route_pitch(experts) * 4;
     return p;
 }
 

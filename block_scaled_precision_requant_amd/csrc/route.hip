@@ -61,6 +61,16 @@ __device__ __forceinline__ float segment_sum(float v) {
         __float_as_uint(v), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
 }
 
+// e^x for x <= 0 (below -200: 0), to about 2 ulp: 2^(x log2 e) with the rounding
+// of the product made good to first order; results under 2^-126 may be 0.
+__device__ __forceinline__ float exp_neg(float x) {
+    x = fmaxf(x, -200.0f);
+    const float t = x * 0x1.715476p+0f;
+    const float r = fmaf(x, 0x1.715476p+0f, -t) + x * 0x1.4ae0cp-26f;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0x1.62e43p-1f, e);
+}
+
 // VPL consecutive logits from element e of a row of `experts` (aligned to the
 // element only); those past the end read as -inf.
 template <int TYPE, int VPL>
@@ -154,15 +164,15 @@ __device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k
     // exp(v - vmax) with equal infinities at distance 0
     auto rel = [&](uint32_t k) {
         const float x = key_logit(k);
-        return k == 0 ? 0.0f : expf(x == vmax ? 0.0f : x - vmax);
+        return k == 0 ? 0.0f : exp_neg(x == vmax ? 0.0f : x - vmax);
     };
     float p;
     if (sigmoid) {
-        // 1 / (1 + e^-v) and e^(v - m) / (1 + e^v); a renormalised row of large
+        // 1 / (1 + e^-v), or e^(v - m) / (1 + e^v) below 0; a renormalised row of large
         // negative logits keeps its ratios through the common factor e^-m
         const float x = key_logit(taken);
         const float m = renorm ? fminf(vmax, 0.0f) : 0.0f;
-        p = taken == 0 ? 0.0f : (x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x - m) / (1.0f + expf(x)));
+        p = taken == 0 ? 0.0f : (x >= 0.0f ? 1.0f : exp_neg(x - m)) / (1.0f + exp_neg(-fabsf(x)));
     } else {
         p = rel(taken);
     }
@@ -291,7 +301,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(
     }
     __syncthreads();
     if (hist != nullptr) {
-        if ((uint32_t)tid < experts) hist[(uint64_t)blockIdx.x * experts + tid] = sh.total[tid];
+        if ((uint32_t)tid < experts) hist[(uint64_t)blockIdx.x * route_pitch(experts) + tid] = sh.total[tid];
         return;
     }
     const uint32_t sum = scan_experts(sh, experts, tid);
@@ -315,27 +325,35 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(
         sh.before[tid] = 0;
     }
     __syncthreads();
-    // the threads of one expert column share the blocks among them
-    uint32_t cols = 64;
-    while (cols < experts) cols *= 2;
-    const uint32_t e = tid % cols, part = tid / cols, parts = kRouteThreads / cols;
+    // a thread adds up four experts over its share of the blocks, 16 loads at a time
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t pitch = route_pitch(experts);
+    uint32_t quads = 16;
+    while (4 * quads < experts) quads *= 2;
+    const uint32_t e = tid % quads * 4, part = tid / quads, parts = kRouteThreads / quads;
     if (e < experts) {
-        uint32_t sum = 0, mine = 0;
+        u32x4 sum = {0, 0, 0, 0}, mine = {0, 0, 0, 0};
         for (uint32_t b0 = part; b0 < gridDim.x; b0 += 16 * parts) {
-            uint32_t c[16];  // 16 loads at a time
+            u32x4 c[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const uint32_t b = b0 + i * parts;
-                c[i] = b < gridDim.x ? hist[(uint64_t)b * experts + e] : 0;
+                c[i] = u32x4{0, 0, 0, 0};
+                if (i * parts >= gridDim.x) continue;  // (the same in all threads)
+                if (b < gridDim.x) c[i] = *reinterpret_cast<const u32x4 *>(hist + (uint64_t)b * pitch + e);
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 sum += c[i];
-                mine += b0 + i * parts < blockIdx.x ? c[i] : 0;
+                if (b0 + i * parts < blockIdx.x) mine += c[i];
             }
         }
-        atomicAdd(&sh.total[e], sum);
-        atomicAdd(&sh.before[e], mine);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e + j < experts) {
+                atomicAdd(&sh.total[e + j], sum[j]);
+                atomicAdd(&sh.before[e + j], mine[j]);
+            }
     }
     __syncthreads();
     const uint32_t sum = scan_experts(sh, experts, tid);
@@ -361,9 +379,9 @@ void launch_select(const void *logits, uint32_t ld, int32_t *ids, float *weights
     if (experts <= 64)
         BSR_ROUTE(4, 16);
     else if (experts <= 128)
-        BSR_ROUTE(4, 32);
+        BSR_ROUTE(8, 16);
     else if (experts <= 256)
-        BSR_ROUTE(4, 64);
+        BSR_ROUTE(8, 32);
     else if (experts <= 512)
         BSR_ROUTE(8, 64);
     else

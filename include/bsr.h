@@ -320,8 +320,8 @@ enum bsr_score {
 };
 
 /*
- * Workspace bytes moe_route needs: 0 for few tokens, never more than
- * 1024 * experts.  Pure host arithmetic, no device call.
+ * Workspace bytes moe_route needs: 0 for few tokens (and for sizes that it
+ * refuses), never more than 1024 * experts.  Pure host arithmetic, no device call.
  */
 BSR_API uint64_t moe_route_ws_bytes(uint32_t tokens, uint32_t experts, uint32_t top_k);
 
@@ -344,7 +344,7 @@ BSR_API uint64_t moe_route_ws_bytes(uint32_t tokens, uint32_t experts, uint32_t 
  * +inf logits share the softmax between them.  A softmax's maximum is taken
  * over the row's logits other than NaN.  The result does not depend on the
  * order in which workgroups run.  tokens == 0 writes offsets (all 0) only.
- *   workspace 4-byte aligned device buffer of at least moe_route_ws_bytes, as
+ *   workspace 16-byte aligned device buffer of at least moe_route_ws_bytes, as
  *             that of int8_gemm_blockscaled_ws: scratch, and not shared by
  *             calls that may overlap in time (NULL where 0 bytes are needed)
  * Limits: 1 <= experts <= 1024, 1 <= top_k <= min(16, experts), tokens * top_k

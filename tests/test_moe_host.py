@@ -38,7 +38,7 @@ W4E = dict(x=FAKE, w=FAKE, scale=FAKE, scale_type=0, zero=None, group=32, offset
     (dict(type=3), INV), (dict(type=-1), INV), (dict(score=2), INV), (dict(scale=float("nan")), INV),
     (dict(scale=float("inf")), INV), (dict(experts=0), INV), (dict(experts=1025, ld=1025), INV), (dict(ld=7), INV),
     (dict(top_k=0), INV), (dict(top_k=9), INV), (dict(top_k=17, experts=64, ld=64), INV),
-    (dict(tokens=1 << 30, top_k=2), INV), (dict(tokens=10000), NUL), (dict(tokens=10000, workspace=_fake(2)), ALI),
+    (dict(tokens=1 << 30, top_k=2), INV), (dict(tokens=10000), NUL), (dict(tokens=10000, workspace=_fake(8)), ALI),
     (dict(tokens=10000, workspace=FAKE, workspace_bytes=16), INV), (dict(offsets=None), NUL),
     (dict(tokens=0, offsets=None), NUL), (dict(logits=None), NUL), (dict(ids=None), NUL), (dict(weights=None), NUL),
     (dict(row_token=None), NUL), (dict(pos=None), NUL), (dict(logits=_fake(2)), ALI), (dict(pos=_fake(2)), ALI),
