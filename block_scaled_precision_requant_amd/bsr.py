@@ -432,3 +432,67 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
     _launch("w4a16_group_gemv_experts", stream, (x_bf16, w_packed, scale, zero, offsets, row_index, out),
             lambda p: (*p[:3], kind, p[3], group, p[4], p[5], int(bool(silu_mul)), p[6], x_bf16.shape[0], rows,
                        lead[0], n, k))
+
+
+class MoeScratch:
+    """What the launches of moe_prefill and moe_decode_w4 pass between them, for up to `tokens` tokens of width
+    `hidden`, `experts` experts of which a token takes `top_k`, and expert projections of width `inter`.  Calls that
+    may overlap in time need one each."""
+
+    def __init__(self, tokens, experts, top_k, hidden, inter, device="cuda"):
+        def buf(*shape, dtype):
+            return torch.zeros(shape, dtype=dtype, device=device)
+        rows = tokens * top_k
+        i32, f32, i8, bf16 = torch.int32, torch.float32, torch.int8, torch.bfloat16
+        self.tokens, self.top_k = tokens, top_k
+        self.ids, self.pos = buf(tokens, top_k, dtype=i32), buf(tokens, top_k, dtype=i32)
+        self.weights = buf(tokens, top_k, dtype=f32)
+        self.offsets, self.row_token = buf(experts + 1, dtype=i32), buf(rows, dtype=i32)
+        self.workspace = buf(1024 * experts, dtype=torch.uint8)
+        self.a_i8, self.a_scale = buf(tokens, hidden, dtype=i8), buf(tokens, hidden // 32, dtype=f32)
+        self.gate_up = buf(rows, 2 * inter, dtype=bf16)
+        self.h_i8, self.h_scale = buf(rows, inter, dtype=i8), buf(rows, inter // 32, dtype=f32)
+        self.h, self.y = buf(rows, inter, dtype=bf16), buf(rows, hidden, dtype=bf16)
+
+    def route(self, logits, **how):
+        """moe_route of the first len(logits) tokens; returns (rows, their buffers' views)."""
+        t = logits.shape[0]
+        if t > self.tokens:
+            raise ValueError(f"{t} tokens, scratch for {self.tokens}")
+        rows = t * self.top_k
+        moe_route(logits, self.ids[:t], self.weights[:t], self.offsets, self.row_token[:rows], self.pos[:t],
+                  self.workspace, **how)
+        return rows
+
+
+def moe_prefill(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale, out, scratch, residual=None,
+                score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
+    """One expert layer on int8 per-32 weights (requant_w_nvfp4_int8 of each expert): x_bf16 [T,H], router logits
+    [T,E], w_gate_up [E,2I,H] (gate rows first), w_down [E,H,I] with their scales -> out [T,H] (+ residual), in six
+    steps on one stream: router, activation requant, grouped gate and up, SiLU product requant, grouped down,
+    weighted sum."""
+    t, inter = x_bf16.shape[0], w_down.shape[2]
+    s = scratch
+    rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
+    a_i8, a_scale, gate_up, y = s.a_i8[:t], s.a_scale[:t], s.gate_up[:rows], s.y[:rows]
+    requant_a_int8(x_bf16, a_i8, a_scale, stream=stream)
+    int8_grouped_gemm_blockscaled(a_i8, w_gate_up, a_scale, gate_up_scale, s.offsets, gate_up,
+                                  row_index=s.row_token[:rows], stream=stream)
+    silu_mul_requant_int8(gate_up[:, :inter], gate_up[:, inter:], s.h_i8[:rows], s.h_scale[:rows], stream=stream)
+    int8_grouped_gemm_blockscaled(s.h_i8[:rows], w_down, s.h_scale[:rows], down_scale, s.offsets, y, stream=stream)
+    moe_combine(y, s.pos[:t], s.weights[:t], out, residual=residual, stream=stream)
+
+
+def moe_decode_w4(x_bf16, logits, w_gate_up, gate_up_scale, gate_up_zero, w_down, down_scale, down_zero, out, scratch,
+                  residual=None, score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
+    """One expert layer on 4-bit weights with group scales, for a few tokens: as moe_prefill, with w_gate_up
+    [E,2I,H/2] and w_down [E,H,I/2] packed, their scales and zero points (or None), in four steps: router, gate and up
+    with the SiLU product, down, weighted sum."""
+    t = x_bf16.shape[0]
+    s = scratch
+    rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
+    h, y = s.h[:rows], s.y[:rows]
+    w4a16_group_gemv_experts(x_bf16, w_gate_up, gate_up_scale, s.offsets, h, zero=gate_up_zero,
+                             row_index=s.row_token[:rows], silu_mul=True, stream=stream)
+    w4a16_group_gemv_experts(h, w_down, down_scale, s.offsets, y, zero=down_zero, stream=stream)
+    moe_combine(y, s.pos[:t], s.weights[:t], out, residual=residual, stream=stream)
