@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsr.so")
-SOURCES = ["requant.hip", "gemm.hip", "gemv.hip", "w4a16.hip", "route.hip", "grouped.hip", "w4_group.hip", "api.hip",
-           "api_moe.hip"]
+SOURCES = ["requant.hip", "gemm.hip", "gemv.hip", "w4a16.hip", "route.hip", "grouped.hip", "grouped_gemv.hip",
+           "w4_group.hip", "api.hip", "api_moe.hip"]
 # The streaming-read kernel bench.py reports as bandwidth context: a library of
 # its own, so libbsr.so exports only the entry points include/bsr.h declares.
 READ_LIB = os.path.join(PKG, "libbsr_read.so")

@@ -10,7 +10,8 @@
 // counts row tiles, wave prefixes give their totals and the tile of this
 // workgroup; workgroups past the total leave.  The tiles are those of
 // gemm_tile.h, their A rows gathered through row_index by the staging itself,
-// so no gathered copy of the activations is made.
+// so no gathered copy of the activations is made.  Few rows per expert run in
+// grouped_gemv.hip instead (grouped_gemv_rule).
 #include "gemm_tile.h"
 #include "moe_internal.h"
 
@@ -151,6 +152,8 @@ __global__ __launch_bounds__(256, 2) void grouped_kernel(
 
 hipError_t launch_grouped_gemm(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
                                const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s) {
+    if (grouped_gemv_rule(g.rows, g.experts, n))
+        return launch_grouped_gemv(a, w, a_s, w_s, out, g, n, k, grouped_gemv_plan(g.rows, g.experts, n, k), s);
     const uint32_t tiles_n = (uint32_t)div_up(n, kGemmBN);
     const uint64_t grid = grouped_row_tiles(g.rows, g.experts, kGemmBM) * tiles_n;
     auto kernel = g.index != nullptr ? gemm_kernels::grouped_kernel<true> : gemm_kernels::grouped_kernel<false>;

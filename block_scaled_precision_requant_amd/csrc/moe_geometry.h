@@ -43,6 +43,56 @@ inline uint64_t grouped_row_tiles(uint32_t rows, uint32_t experts, uint32_t bm) 
     return (rows + used * (bm - 1)) / bm;
 }
 
+// ---- grouped GEMV (few rows per expert) -------------------------------------
+// A workgroup owns 16 output columns and a tile of up to 16 rows, or 4; its
+// waves split K in chunks of 128 bytes, two to a pass.
+constexpr uint32_t kGgCols = 16;
+constexpr uint32_t kGgRows = 16;
+constexpr uint32_t kGgFew = 4;
+constexpr uint32_t kGgChunk = 128;
+constexpr uint32_t kGgPass = 2;
+// 16 waves leave a wave 128 registers, which tiles of 4 rows fit.
+BSR_HD constexpr uint32_t gg_max_waves(uint32_t rows) { return rows <= kGgFew ? 16 : 8; }
+// LDS bytes of a wave: its pass's activation rows (16 bytes of padding spread
+// 16 rows over the banks) and their scales, [block][row].
+BSR_HD constexpr uint32_t gg_pitch() { return kGgPass * kGgChunk + 16; }
+BSR_HD constexpr uint32_t gg_wave_bytes(uint32_t rows) { return rows * (gg_pitch() + kGgPass * 4 * 4); }
+
+// The GEMV runs for one row per used expert on average, and for more while the
+// GEMM's 128 x 128 tiles would leave CUs idle.  Measured (GEMV against GEMM, us;
+// experts, n, k): 8, 4096, 14336 at 1 / 4 / 8 / 16 rows each 80 / 114 / 132 / 165 against
+// 116 / 126 / 127 / 127; 16, 512, 4096 at 1 / 16 rows 8.8 / 18.7 against 28 / 40;
+// 64, 4096, 2048 at 1 / 2 / 4 rows 67 / 91 / 113 against 71 / 84 / 109.
+inline bool grouped_gemv_rule(uint32_t rows, uint32_t experts, uint32_t n) {
+    const uint64_t used = rows < experts ? rows : experts;
+    const uint64_t tiles = grouped_row_tiles(rows, experts, kGemmBM) * div_up(n, kGemmBN);
+    return rows <= used || rows * tiles <= 6 * kGemmCus * used;
+}
+
+struct GroupedGemvPlan {
+    uint32_t rows, row_tiles, col_tiles, waves, chunks_per_wave, lds;
+};
+
+inline GroupedGemvPlan grouped_gemv_plan(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k) {
+    GroupedGemvPlan p;
+    const uint32_t used = rows < experts ? rows : experts;
+    p.rows = rows <= kGgFew || rows <= 2 * (uint64_t)used ? kGgFew : kGgRows;
+    const uint32_t chunks = (uint32_t)div_up(k, kGgChunk);
+    p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, p.rows);
+    p.col_tiles = (uint32_t)div_up(n, kGgCols);
+    const uint32_t most = gg_max_waves(p.rows);
+    uint64_t waves = most * (uint64_t)kGemmCus / ((uint64_t)p.row_tiles * p.col_tiles);  // what runs at once
+    waves = waves > 1 ? waves : 1;
+    waves = waves < most ? waves : most;
+    waves = waves < chunks ? waves : chunks;
+    p.chunks_per_wave = (uint32_t)div_up(div_up(chunks, waves), kGgPass) * kGgPass;  // whole passes
+    p.waves = (uint32_t)div_up(chunks, p.chunks_per_wave);
+    p.lds = p.waves * gg_wave_bytes(p.rows);
+    const uint32_t sums = p.waves * 64 * 4 * 4;
+    p.lds = p.lds > sums ? p.lds : sums;
+    return p;
+}
+
 // ---- 4-bit group GEMV -------------------------------------------------------
 // A workgroup owns a tile of up to 16 rows, or 4, and 16 output columns, 32
 // (`ct` tiles of 16), or with the SiLU product 16 of the gate and 16 of the up

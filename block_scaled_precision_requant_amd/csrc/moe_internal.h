@@ -38,6 +38,10 @@ struct GroupedRows {
 
 hipError_t launch_grouped_gemm(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
                                const GroupedRows &g, uint32_t n, uint32_t k, hipStream_t s);
+// The same for few rows per expert (plan from grouped_gemv_plan).
+hipError_t launch_grouped_gemv(const int8_t *a, const int8_t *w, const float *a_s, const float *w_s, uint16_t *out,
+                               const GroupedRows &g, uint32_t n, uint32_t k, const GroupedGemvPlan &plan,
+                               hipStream_t s);
 hipError_t launch_w4_group(const uint16_t *x, const uint8_t *w, const void *scale, int scale_type,
                            const uint8_t *zero, uint32_t group, uint16_t *out, const GroupedRows &g, bool silu,
                            uint32_t n, uint32_t k, hipStream_t s);
@@ -90,6 +94,27 @@ struct RowTiles {
         }
     }
 };
+
+// ---- streamed weights (the two GEMVs) ----
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+// Lane (c, q) holds dword j of quarter q in component j -> dword q of quarter j:
+// a 4 x 4 transposition over the four rows of 16 lanes.
+__device__ __forceinline__ v4i swap_quarters(v4i w) {
+    const auto a = __builtin_amdgcn_permlane16_swap((uint32_t)w.x, (uint32_t)w.y, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap((uint32_t)w.z, (uint32_t)w.w, false, false);
+    const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+    return v4i{(int)c[0], (int)d[0], (int)c[1], (int)d[1]};
+}
+
+constexpr int kRsrcWord3 = 0x00020000;         // raw buffer (gfx9)
+constexpr uint32_t kPastEnd = 0xFFFFFFE0u;     // an offset behind every buffer: reads as 0
+
+__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, uint32_t offset) {
+    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0));
+}
 
 // Operand row of output row p, or -1 for a row of zeros.
 __device__ __forceinline__ int32_t source_row(const GroupedRows &g, uint32_t p) {

@@ -22,8 +22,6 @@
 namespace bsr {
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // Eight codes -> BF16 16 + c, pairs (0,4) (1,5) (2,6) (3,7); mask = 0x00780078.
@@ -40,16 +38,6 @@ __device__ __forceinline__ v4i pair_order(v4i x) {
                (int)__builtin_amdgcn_perm((uint32_t)x.z, (uint32_t)x.x, 0x07060302u),
                (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.y, 0x05040100u),
                (int)__builtin_amdgcn_perm((uint32_t)x.w, (uint32_t)x.y, 0x07060302u)};
-}
-
-// Lane (c, q) holds dword j of quarter q in component j -> dword q of quarter j:
-// a 4 x 4 transposition over the four rows of 16 lanes.
-__device__ __forceinline__ v4i swap_quarters(v4i w) {
-    const auto a = __builtin_amdgcn_permlane16_swap((uint32_t)w.x, (uint32_t)w.y, false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap((uint32_t)w.z, (uint32_t)w.w, false, false);
-    const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
-    return v4i{(int)c[0], (int)d[0], (int)c[1], (int)d[1]};
 }
 
 // N consecutive elements of BYTES each, loaded as wide as they come wherever
@@ -123,13 +111,6 @@ struct Pass {
     Run<kScaleBytes<STYPE>, kGroups> s[CT];
     Run<1, kGroups> z[CT];
 };
-
-constexpr int kRsrcWord3 = 0x00020000;         // raw buffer (gfx9)
-constexpr uint32_t kPastEnd = 0xFFFFFFE0u;     // an offset behind every buffer: reads as 0
-
-__device__ __forceinline__ v4i load16(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, uint32_t offset) {
-    return __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(r, lane_offset, offset, 0));
-}
 
 struct W4Args {
     const uint16_t *x;

@@ -304,3 +304,11 @@ def test_combine(tokens, top_k, rows, n, residual, shift):
         rr = placed(r)
         bsr.moe_combine(placed(y), to_dev(pos), to_dev(w), rr, residual=rr)
         assert np.array_equal(host(rr), host(out))
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("rows, experts, n, k, kind", [
+    # the GEMV of few rows per expert: tiles of 4 and of 16 rows, K split over 1 to 16 waves, chunks cut short
+    (4, 2, 16, 32, "even"), (3, 9, 17, 224, "random"), (7, 7, 4096, 128, "random"), (8, 2, 300, 14336, "random"),
+    (33, 2, 100, 4128, "random"), (90, 6, 130, 1120, "holes"), (64, 4, 128, 2048, "one"), (16, 16, 512, 4096, "holes"),
+    (2, 2, 28672, 256, "even"), (140, 9, 72, 96, "random")])
+def test_grouped_few_rows(rows, experts, n, k, kind, gather):
+    test_grouped(rows, experts, n, k, kind, gather)

@@ -131,9 +131,10 @@ def test_scratch_serves_fewer_tokens_and_refuses_more():
     layer = _Layer(3, 40, 8, 2, 256, 128)
     out = layer.outs()[0]
     layer.prefill(out)
-    fewer = torch.empty_like(out[:7])
-    bsr.moe_prefill(layer.x[:7], layer.logits[:7], *layer.i8, fewer, layer.scratch, residual=layer.residual[:7])
-    assert torch.equal(fewer.view(torch.int16), out[:7].view(torch.int16))  # a row's bits do not depend on the others
+    fewer, own = torch.empty_like(out[:7]), torch.empty_like(out[:7])
+    for o, scratch in ((fewer, layer.scratch), (own, bsr.MoeScratch(7, 8, 2, 256, 128))):
+        bsr.moe_prefill(layer.x[:7], layer.logits[:7], *layer.i8, o, scratch, residual=layer.residual[:7])
+    assert torch.equal(fewer.view(torch.int16), own.view(torch.int16))
     with pytest.raises(ValueError, match="41 tokens"):
         layer.scratch.route(torch.zeros((41, 8), device=DEV))
 
