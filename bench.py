@@ -46,7 +46,7 @@ PEAK_INT8_TOPS = 5000.0        # MI355X dense int8 MFMA
 PEAK_VALU_TOPS = 157.3 / 2                     # FP32 vector peak 157.3 TFLOP/s as FMA lane operations (T/s)
 PEAK_HBM_GBS = 8000.0          # MI355X HBM3E
 PROFILE_COUNTERS = os.path.join(ROOT, "profiles", "hbm_traffic.json")
-GEMM_SOURCES = ["gemm.hip", "bsr_internal.h", "bsr_geometry.h"]
+GEMM_SOURCES = ["gemm.hip", "gemm_tile.h", "bsr_internal.h", "bsr_geometry.h"]
 RQ_SOURCES = ["requant.hip", "bsr_internal.h", "bsr_geometry.h"]
 
 

@@ -74,6 +74,10 @@ struct Run {
             }
         }
     }
+    __device__ __forceinline__ void fill(uint32_t word) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) raw[i] = word;
+    }
     // the first `live` entries; the others are 0
     __device__ __forceinline__ void load_some(const uint8_t *from, uint32_t live) {
 #pragma unroll
@@ -185,6 +189,7 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
                     b.s[ct].load_some(sp, groups - g0);
                     if (p.zero != nullptr) b.z[ct].load_some(zp, groups - g0);
                 }
+                if (p.zero == nullptr) b.z[ct].fill(0x08080808u);
             }
         }
 #pragma unroll
@@ -241,7 +246,7 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
                                                                        psum[ct], 0, 0, 0);
                     if (GPC > 0 && j % per == per - 1) {
                         const float s = scale_value<STYPE>(b.s[ct].bits(i * GPC + j / per));
-                        const float z = p.zero != nullptr ? (float)b.z[ct].bits(i * GPC + j / per) : 8.0f;
+                        const float z = (float)b.z[ct].bits(i * GPC + j / per);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             acc[ct][r] = fmaf(s, fmaf(-16.0f - z, xsum[r], psum[ct][r]), acc[ct][r]);

@@ -31,8 +31,8 @@ COPY_BYTES = 256 * 2 ** 20
 
 # Source files each kernel family is built from (the digest bench.py checks).
 SOURCES = {
-    "gemm_kernel": ["gemm.hip", "bsr_internal.h", "bsr_geometry.h"],
-    "split_reduce_kernel": ["gemm.hip", "bsr_internal.h", "bsr_geometry.h"],
+    "gemm_kernel": ["gemm.hip", "gemm_tile.h", "bsr_internal.h", "bsr_geometry.h"],
+    "split_reduce_kernel": ["gemm.hip", "gemm_tile.h", "bsr_internal.h", "bsr_geometry.h"],
     "requant_w_kernel": ["requant.hip", "bsr_internal.h", "bsr_geometry.h"],
     "requant_a_kernel": ["requant.hip", "bsr_internal.h", "bsr_geometry.h"],
     "silu_requant": ["requant.hip", "bsr_internal.h", "bsr_geometry.h"],
