@@ -298,28 +298,36 @@ def _type(t, what):
     return TYPE_BF16
 
 
-def _launch(name, stream, tensors, args):
-    """Calls an entry point with the data pointers of `tensors` (None: NULL), the other arguments and a stream
-    (default: torch's current one on the tensors' device), that device being the current one during the call.
-    Small decode calls last as long as this does, so it takes the short ways: integers for devices and pointers."""
-    dev = tensors[0].get_device()
-    ptrs = []
-    for t in tensors:
-        if t is None:
-            ptrs.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError(f"arguments on {tensors[0].device} and {t.device}: all must be on one device")
-        ptrs.append(t.data_ptr())
+# Small decode calls last as long as the host takes to issue them, so the calls
+# below look at each tensor once and take the short ways: integers for devices
+# and pointers.
+
+def _arg(t, shape, kind, what, dev):
+    """Data pointer of a contiguous tensor of this shape and element kind on device `dev`."""
+    if t.shape != shape or t.dtype not in _USUAL[kind] or not t.is_contiguous() or t.get_device() != dev:
+        _shape(t, shape, what, kind)
+        _same_device(t, what, dev)
+    return t.data_ptr()
+
+
+def _same_device(t, what, dev):
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, the other arguments on "
+                         f"{'the CPU' if dev < 0 else f'cuda:{dev}'}: all must be on one device")
+
+
+def _launch(name, dev, stream, *args):
+    """Calls an entry point with `args` and a stream (default: torch's current one on device `dev`), `dev` being
+    the current device during the call."""
     if dev < 0:
         raise ValueError("arguments must be device tensors")
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     fn = getattr(_LIB or lib(), name)
-    if torch.cuda.current_device() == dev:
-        status = fn(*args(ptrs), raw)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args(ptrs), raw)
+            status = fn(*args, raw)
     if status != BSR_OK:
         raise BsrError(status, name)
 
@@ -341,25 +349,26 @@ def moe_route(logits, ids, weights, offsets, row_token, pos, workspace=None, sco
     kind = _type(logits, "logits")
     if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
         raise ValueError("logits: rows with unit column stride that do not overlap")
-    for x, shape, what, dt in ((ids, (t, k), "ids", I32), (weights, (t, k), "weights", F32),
-                               (offsets, (e + 1,), "offsets", I32), (row_token, (t * k,), "row_token", I32),
-                               (pos, (t, k), "pos", I32)):
-        _shape(x, shape, what, dt)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    ld = logits.stride(0) if t > 1 else e
-    _launch("moe_route", stream, (logits, ids, weights, offsets, row_token, pos, workspace),
-            lambda p: (p[0], kind, ld, *p[1:6], t, e, k, int(score), int(bool(renorm)), float(scale), p[6], ws_bytes))
+    dev = logits.get_device()
+    ptrs = (_arg(ids, (t, k), I32, "ids", dev), _arg(weights, (t, k), F32, "weights", dev),
+            _arg(offsets, (e + 1,), I32, "offsets", dev), _arg(row_token, (t * k,), I32, "row_token", dev),
+            _arg(pos, (t, k), I32, "pos", dev))
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        _same_device(workspace, "workspace", dev)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch("moe_route", dev, stream, logits.data_ptr(), kind, logits.stride(0) if t > 1 else e, *ptrs, t, e, k, score,
+            1 if renorm else 0, scale, ws, ws_bytes)
 
 
-def _grouped_shapes(offsets, row_index, out, cols, experts):
+def _rows_args(offsets, row_index, out, cols, experts, dev):
+    """Pointers of (offsets, row_index or NULL, out) of a grouped call, and its row capacity."""
     rows = out.shape[0]
-    _shape(out, (rows, cols), "out", BF16)
-    _shape(offsets, (experts + 1,), "offsets", I32)
-    if row_index is not None:
-        _shape(row_index, (rows,), "row_index", I32)
-    return rows
+    return (_arg(offsets, (experts + 1,), I32, "offsets", dev),
+            None if row_index is None else _arg(row_index, (rows,), I32, "row_index", dev),
+            _arg(out, (rows, cols), BF16, "out", dev), rows)
 
 
 def int8_grouped_gemm_blockscaled(a_i8, w_i8, a_scale, w_scale, offsets, out, row_index=None, stream=None):
@@ -367,13 +376,12 @@ def int8_grouped_gemm_blockscaled(a_i8, w_i8, a_scale, w_scale, offsets, out, ro
     of a_i8 [A,K] / a_scale [A,K/32] times the weight w_i8 [E,N,K] / w_scale [E,N,K/32] of expert e."""
     a_rows, k = a_i8.shape
     e, n, _ = w_i8.shape
-    _shape(a_i8, (a_rows, k), "a_i8", BYTES)
-    _shape(w_i8, (e, n, k), "w_i8", BYTES)
-    _shape(a_scale, (a_rows, k // 32), "a_scale", F32)
-    _shape(w_scale, (e, n, k // 32), "w_scale", F32)
-    rows = _grouped_shapes(offsets, row_index, out, n, e)
-    _launch("int8_grouped_gemm_blockscaled", stream, (a_i8, w_i8, a_scale, w_scale, offsets, row_index, out),
-            lambda p: (*p, a_rows, rows, e, n, k))
+    dev = a_i8.get_device()
+    a, w = _arg(a_i8, (a_rows, k), BYTES, "a_i8", dev), _arg(w_i8, (e, n, k), BYTES, "w_i8", dev)
+    a_s = _arg(a_scale, (a_rows, k // 32), F32, "a_scale", dev)
+    w_s = _arg(w_scale, (e, n, k // 32), F32, "w_scale", dev)
+    off, index, o, rows = _rows_args(offsets, row_index, out, n, e, dev)
+    _launch("int8_grouped_gemm_blockscaled", dev, stream, a, w, a_s, w_s, off, index, o, a_rows, rows, e, n, k)
 
 
 def moe_combine(y, pos, weights, out, residual=None, stream=None):
@@ -381,43 +389,40 @@ def moe_combine(y, pos, weights, out, residual=None, stream=None):
     0..R-1 adds nothing)."""
     rows, n = y.shape
     t, k = pos.shape
-    _shape(y, (rows, n), "y", BF16)
-    _shape(pos, (t, k), "pos", I32)
-    _shape(weights, (t, k), "weights", F32)
-    _shape(out, (t, n), "out", BF16)
-    if residual is not None:
-        _shape(residual, (t, n), "residual", BF16)
-    _launch("moe_combine", stream, (y, pos, weights, residual, out), lambda p: (*p, t, k, rows, n))
+    dev = y.get_device()
+    _launch("moe_combine", dev, stream, _arg(y, (rows, n), BF16, "y", dev), _arg(pos, (t, k), I32, "pos", dev),
+            _arg(weights, (t, k), F32, "weights", dev),
+            None if residual is None else _arg(residual, (t, n), BF16, "residual", dev),
+            _arg(out, (t, n), BF16, "out", dev), t, k, rows, n)
 
 
-def _w4_shapes(x, w_packed, scale, zero):
-    """(lead, n, k, group, scale type) of a 4-bit weight w_packed [*lead, N, K/2] for x [M, K]."""
-    k = x.shape[1]
-    lead, n = tuple(w_packed.shape[:-2]), w_packed.shape[-2]
-    _shape(x, (x.shape[0], k), "x_bf16", BF16)
-    _shape(w_packed, lead + (n, k // 2), "w_packed", BYTES)
+def _w4_args(x, w_packed, scale, zero, dims, dev):
+    """Pointers of (x, w_packed, scale), the scale type, the pointer of zero, the group, and (lead, n, k), of a 4-bit
+    weight w_packed [*lead, N, K/2] of `dims` dimensions for x [M, K]."""
+    m, k = x.shape
+    if w_packed.dim() != dims:
+        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected {('two', 'three')[dims - 2]} dimensions")
+    lead, n = w_packed.shape[:-2], w_packed.shape[-2]
     cols = scale.shape[-1]
     if cols == 0 or k % cols:
         raise ValueError(f"scale: {cols} groups do not divide K = {k}")
-    kind = _type(scale, "scale")
-    if scale.shape != lead + (n, cols) or not scale.is_contiguous():
-        raise ValueError(f"scale: shape {tuple(scale.shape)}, expected contiguous {lead + (n, cols)}")
-    if zero is not None:
-        _shape(zero, lead + (n, cols), "zero", BYTES)
-    return lead, n, k, 0 if cols == 1 else k // cols, kind
+    kind, shape = _type(scale, "scale"), (*lead, n, cols)
+    if scale.shape != shape or not scale.is_contiguous():
+        raise ValueError(f"scale: shape {tuple(scale.shape)}, expected contiguous {shape}")
+    _same_device(scale, "scale", dev)
+    ptrs = (_arg(x, (m, k), BF16, "x_bf16", dev), _arg(w_packed, (*lead, n, k // 2), BYTES, "w_packed", dev),
+            scale.data_ptr(), kind, None if zero is None else _arg(zero, shape, BYTES, "zero", dev),
+            0 if cols == 1 else k // cols)
+    return ptrs, lead, n, k
 
 
 def w4a16_group_gemv(x_bf16, w_packed, scale, out, zero=None, stream=None):
     """out [M,N] BF16 = x_bf16 [M,K] times the 4-bit weight scale * (code - zero): w_packed [N,K/2] (low nibble
     first), scale [N,K/group] (BF16, float16 or float32; one column: one scale per row), zero [N,K/group] uint8 or
     None (8 throughout)."""
-    lead, n, k, group, kind = _w4_shapes(x_bf16, w_packed, scale, zero)
-    if lead:
-        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected two dimensions")
-    m = x_bf16.shape[0]
-    _shape(out, (m, n), "out", BF16)
-    _launch("w4a16_group_gemv", stream, (x_bf16, w_packed, scale, zero, out),
-            lambda p: (*p[:3], kind, p[3], group, p[4], m, n, k))
+    dev, m = x_bf16.get_device(), x_bf16.shape[0]
+    ptrs, _, n, k = _w4_args(x_bf16, w_packed, scale, zero, 2, dev)
+    _launch("w4a16_group_gemv", dev, stream, *ptrs, _arg(out, (m, n), BF16, "out", dev), m, n, k)
 
 
 def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, row_index=None, silu_mul=False,
@@ -425,13 +430,11 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
     """w4a16_group_gemv by expert (w_packed [E,N,K/2], scale and zero [E,N,K/group]); offsets and row_index as
     int8_grouped_gemm_blockscaled.  silu_mul: the first N/2 columns are gates, the others ups, and out [R,N/2] is
     SiLU(gate) * up."""
-    lead, n, k, group, kind = _w4_shapes(x_bf16, w_packed, scale, zero)
-    if len(lead) != 1:
-        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected three dimensions")
-    rows = _grouped_shapes(offsets, row_index, out, n // 2 if silu_mul else n, lead[0])
-    _launch("w4a16_group_gemv_experts", stream, (x_bf16, w_packed, scale, zero, offsets, row_index, out),
-            lambda p: (*p[:3], kind, p[3], group, p[4], p[5], int(bool(silu_mul)), p[6], x_bf16.shape[0], rows,
-                       lead[0], n, k))
+    dev = x_bf16.get_device()
+    ptrs, (e,), n, k = _w4_args(x_bf16, w_packed, scale, zero, 3, dev)
+    off, index, o, rows = _rows_args(offsets, row_index, out, n // 2 if silu_mul else n, e, dev)
+    _launch("w4a16_group_gemv_experts", dev, stream, *ptrs, off, index, 1 if silu_mul else 0, o, x_bf16.shape[0], rows,
+            e, n, k)
 
 
 class MoeScratch:

@@ -24,7 +24,8 @@ bool type_ok(int type) { return type == BSR_TYPE_BF16 || type == BSR_TYPE_F16 ||
 
 // Shapes the grouped calls share; `src_rows` operand rows.
 bool grouped_ok(const int32_t *row_index, uint32_t src_rows, uint32_t rows, uint32_t experts) {
-    return rows <= kMaxRows && experts <= kMaxExperts && (row_index != nullptr || src_rows >= rows);
+    return rows <= kMaxRows && experts <= kMaxExperts &&
+           (row_index != nullptr ? src_rows != 0 || rows == 0 : src_rows >= rows);
 }
 
 int w4_check(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type, const uint16_t *out) {

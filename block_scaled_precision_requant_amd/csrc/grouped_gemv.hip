@@ -80,12 +80,21 @@ __global__ __launch_bounds__(gg_max_waves(ROWS) * 64) void grouped_gemv_kernel(
     float *qs = reinterpret_cast<float *>(xs + ROWS * kPitch);  // [block][row]
     v4i xv[kLoads];
     float qv[kScaleLoads];
-    auto load = [&](Pass &b, uint32_t chunk) __attribute__((always_inline)) {
+    // (in a pass cut short scalar offsets stay inside a row, and scales come one
+    // by one, so that a buffer's end bounds every load)
+    auto load = [&](Pass &b, uint32_t chunk, bool part) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < (int)PC; ++i) {
-            b.s[i] = load16(rs, so, (chunk + i) * 16);
+            const uint32_t at = min(chunk + i, part ? chunks - 1 : ~0u);
+            if (!part) {
+                b.s[i] = load16(rs, so, at * 16);
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) b.w[i][h] = load16(rw, wo + 16 * h, (chunk + i) * kGgChunk);
+                for (int j = 0; j < 4; ++j)
+                    b.s[i][j] = (int)__builtin_amdgcn_raw_buffer_load_b32(rs, so + 4 * j, at * 16, 0);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) b.w[i][h] = load16(rw, wo + 16 * h, at * kGgChunk);
         }
     };
     // past K in a pass cut short the activations and their scales are 0
@@ -136,7 +145,7 @@ __global__ __launch_bounds__(gg_max_waves(ROWS) * 64) void grouped_gemv_kernel(
         store_x();
         if (more) {
             load_x(chunk + PC, false);
-            load(next, chunk + PC);
+            load(next, chunk + PC, false);
         }
         compute(b, PC);
     };
@@ -146,7 +155,7 @@ __global__ __launch_bounds__(gg_max_waves(ROWS) * 64) void grouped_gemv_kernel(
     uint32_t chunk = first;
     if (passes > 0) {
         load_x(chunk, false);
-        load(b0, chunk);
+        load(b0, chunk, false);
         const uint32_t last = first + (passes - 1) * PC;
         for (;;) {
             if (chunk == last) {
@@ -166,7 +175,7 @@ __global__ __launch_bounds__(gg_max_waves(ROWS) * 64) void grouped_gemv_kernel(
     }
     if (chunk < end) {
         load_x(chunk, true);
-        load(b0, chunk);
+        load(b0, chunk, true);
         store_x();
         compute(b0, end - chunk);
     }

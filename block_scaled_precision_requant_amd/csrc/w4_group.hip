@@ -141,20 +141,22 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
     const uint32_t first = wave * p.chunks_per_wave, end = min(chunks, first + p.chunks_per_wave);
     // Addresses: a descriptor or base pointer that is the same in all lanes, a
     // 32-bit offset per lane that stays, and the pass's offset as a scalar.
-    // Weight rows past the last column, and bytes past the buffer, read as 0.
+    // Weight rows past the last column read as 0; scalar offsets stay inside a
+    // row, so that a buffer's end bounds every load.
     __amdgpu_buffer_rsrc_t rw[CT];
     const uint8_t *sbase[CT], *zbase[CT];
     uint32_t srow[CT];  // scale row within the tile
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-        const uint32_t c0 = SILU ? col0 : col0 + ct * kW4gCols;  // (CT 2: the second tile may lie past the end)
-        const uint32_t live = c0 < p.cols ? min(p.cols - c0, kW4gCols) : 0;
+        // (CT 2: a second tile past the end reads the last row and is not written)
+        const uint32_t c0 = SILU ? col0 : col0 + ct * kW4gCols;
+        const uint32_t live = c0 < p.cols ? min(p.cols - c0, kW4gCols) : 1;
         const uint64_t row = (uint64_t)t.expert * p.n + (SILU ? ct * p.cols : 0) + min(c0, p.cols - 1);
         rw[ct] = __builtin_amdgcn_make_buffer_rsrc((void *)(p.w + row * (p.k / 2)), (short)0, (int)(live * (p.k / 2)),
                                                    kRsrcWord3);
         sbase[ct] = static_cast<const uint8_t *>(p.scale) + row * groups * kScaleBytes<STYPE>;
         zbase[ct] = p.zero + row * groups;
-        srow[ct] = live == 0 ? 0 : min(c, live - 1);
+        srow[ct] = min(c, live - 1);
     }
     const uint32_t wo = c * (p.k / 2) + 16 * q;
 
@@ -196,7 +198,7 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
         for (int i = 0; i < PC; ++i)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
-                b.w[ct][i] = load16(rw[ct], wo, (chunk + i) * (kW4gChunk / 2));
+                b.w[ct][i] = load16(rw[ct], wo, min(chunk + i, part ? chunks - 1 : ~0u) * (kW4gChunk / 2));
     };
     auto load_x = [&](uint32_t chunk, bool part) __attribute__((always_inline)) {
         const bool live = !part || chunk * kW4gChunk + xk < p.k;

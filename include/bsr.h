@@ -368,12 +368,15 @@ BSR_API int moe_route(const void *logits, int type, uint32_t ld, int32_t *ids, f
  *   w_scale [experts, n, k/32]  f32,  4-byte aligned
  *   offsets [experts + 1]       i32,  4-byte aligned (see above)
  *   row_index [rows] i32 (moe_route's row_token) or NULL; an entry outside
- *           [0, a_rows) stands for a row of zeros.  NULL needs a_rows >= rows
+ *           [0, a_rows) stands for a row of zeros.  NULL needs a_rows >= rows,
+ *           row_index a_rows >= 1
  *   out     [rows, n]           BF16 as raw u16, 2-byte aligned
  * `rows` is the row capacity (tokens * top_k); offsets says how many are used.
+ * Scales must be finite, as for int8_gemm_blockscaled.  The FP32 summation
+ * order follows the sizes of the call; equal calls give equal bits.
  * Limits: experts <= 65536, rows < 2^31, k < 2^24, and with row_index a_rows *
  * k < 2^32 (the rows are gathered with 32-bit offsets).
- * Errors: BSR_EINVAL (k, those limits, a_rows < rows without row_index),
+ * Errors: BSR_EINVAL (k, those limits, a_rows too small, too many workgroups),
  * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  rows == 0, n == 0 or
  * experts == 0 is a valid empty problem.
  */
@@ -432,8 +435,8 @@ BSR_API int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const v
  *            bf16_rne( fl32(gate / fl32(1 + exp(-gate))) * up ), gate and up in
  *            binary32; n must be even
  * Limits: experts <= 65536, rows < 2^31, k < 2^24, x_rows * k < 2^31.
- * Errors: as w4a16_group_gemv; BSR_EINVAL too for x_rows < rows without
- * row_index, silu_mul other than 0 or 1, an odd n with it, and those limits.
+ * Errors: as w4a16_group_gemv; BSR_EINVAL too for x_rows too small (as a_rows
+ * there), silu_mul other than 0 or 1, an odd n with it, and those limits.
  */
 BSR_API int w4a16_group_gemv_experts(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type,
                                      const uint8_t *zero, uint32_t group, const int32_t *offsets,

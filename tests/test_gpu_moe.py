@@ -195,7 +195,10 @@ W4 = [  # m, n, k, group, scale type, zero points
     (4, 512, 4096, 128, "bf16", "4 bit"), (8, 96, 1056, 32, "f16", None), (16, 256, 2048, 32, "f32", "4 bit"),
     (9, 4096, 256, 64, "bf16", "4 bit"), (40, 80, 640, 128, "f16", None), (1, 14336, 384, 128, "bf16", "4 bit"),
     (16, 1000, 14336, 32, "f16", None), (2, 50, 14336, 0, "bf16", "any"), (7, 333, 4480, 64, "f32", "any"),
-    (1, 4096, 6144, 128, "f16", "4 bit"), (33, 65, 96, 0, "f16", None)]
+    (1, 4096, 6144, 128, "f16", "4 bit"), (33, 65, 96, 0, "f16", None),
+    # two column tiles a workgroup, the last one of 1 or 8 columns; one column, chunks cut short
+    (5, 8200, 160, 32, "bf16", "any"), (16, 8193, 96, 32, "f16", None), (12, 8225, 448, 64, "f32", "4 bit"),
+    (1, 1, 1440, 32, "f32", "4 bit"), (16, 1, 288, 32, "bf16", "any"), (4, 17, 704, 64, "f16", "any")]
 
 
 @pytest.mark.parametrize("m, n, k, group, kind, zero", W4)
@@ -309,6 +312,7 @@ def test_combine(tokens, top_k, rows, n, residual, shift):
     # the GEMV of few rows per expert: tiles of 4 and of 16 rows, K split over 1 to 16 waves, chunks cut short
     (4, 2, 16, 32, "even"), (3, 9, 17, 224, "random"), (7, 7, 4096, 128, "random"), (8, 2, 300, 14336, "random"),
     (33, 2, 100, 4128, "random"), (90, 6, 130, 1120, "holes"), (64, 4, 128, 2048, "one"), (16, 16, 512, 4096, "holes"),
-    (2, 2, 28672, 256, "even"), (140, 9, 72, 96, "random")])
+    (2, 2, 28672, 256, "even"), (140, 9, 72, 96, "random"), (1, 1, 1, 1440, "even"), (5, 1, 17, 416, "even"),
+    (16, 1, 1, 160, "even")])
 def test_grouped_few_rows(rows, experts, n, k, kind, gather):
     test_grouped(rows, experts, n, k, kind, gather)

@@ -135,6 +135,10 @@ def test_scratch_serves_fewer_tokens_and_refuses_more():
     for o, scratch in ((fewer, layer.scratch), (own, bsr.MoeScratch(7, 8, 2, 256, 128))):
         bsr.moe_prefill(layer.x[:7], layer.logits[:7], *layer.i8, o, scratch, residual=layer.residual[:7])
     assert torch.equal(fewer.view(torch.int16), own.view(torch.int16))
+    for path in (lambda *a, **k: bsr.moe_prefill(*a[:2], *layer.i8, *a[2:], **k),
+                 lambda *a, **k: bsr.moe_decode_w4(*a[:2], *layer.w4, *a[2:], **k)):  # no tokens at all
+        path(layer.x[:0], layer.logits[:0], out[:0], layer.scratch, residual=layer.residual[:0])
+        assert layer.scratch.offsets.tolist() == [0] * 9
     with pytest.raises(ValueError, match="41 tokens"):
         layer.scratch.route(torch.zeros((41, 8), device=DEV))
 

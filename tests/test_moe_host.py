@@ -51,7 +51,7 @@ def test_route_refusals(change, status):
 
 @pytest.mark.parametrize("change, status", [
     (dict(k=0), INV), (dict(k=48), INV), (dict(k=1 << 24), INV), (dict(experts=65537), INV), (dict(rows=1 << 31), INV),
-    (dict(rows=5), INV), (dict(row_index=FAKE, a_rows=1 << 26, k=64), INV), (dict(rows=0), OK), (dict(n=0), OK),
+    (dict(rows=5), INV), (dict(row_index=FAKE, a_rows=0), INV), (dict(row_index=FAKE, a_rows=1 << 26, k=64), INV), (dict(rows=0), OK), (dict(n=0), OK),
     (dict(experts=0), OK), (dict(a=None), NUL), (dict(w=None), NUL), (dict(a_s=None), NUL), (dict(w_s=None), NUL),
     (dict(offsets=None), NUL), (dict(out=None), NUL), (dict(a=_fake(8)), ALI), (dict(w=_fake(8)), ALI),
     (dict(a_s=_fake(2)), ALI), (dict(w_s=_fake(2)), ALI), (dict(offsets=_fake(2)), ALI),
@@ -88,6 +88,7 @@ def test_w4_group_refusals(change, status):
 
 @pytest.mark.parametrize("change, status", W4_BOTH + [
     (dict(rows=0), OK), (dict(experts=0), OK), (dict(rows=5), INV), (dict(experts=65537), INV), (dict(silu_mul=2), INV),
+    (dict(row_index=FAKE, x_rows=0), INV),
     (dict(silu_mul=1, n=7), INV), (dict(offsets=None), NUL), (dict(offsets=_fake(2)), ALI),
     (dict(row_index=_fake(2)), ALI), (dict(rows=1 << 31), INV), (dict(x_rows=1 << 25), INV),
 ])
