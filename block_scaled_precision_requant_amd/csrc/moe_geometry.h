@@ -15,6 +15,9 @@ constexpr uint32_t kRouteMaxTopK = 16;
 constexpr uint32_t kRouteThreads = 1024;
 constexpr uint32_t kRouteWaves = kRouteThreads / 64;
 constexpr uint32_t kRouteMaxBlocks = 256;
+// One workgroup alone takes up to this many tokens (64 x 64 experts, top 8: 6.3 us,
+// in two launches 8.1; 128 x 128, top 4: 9.4 and 8.3); more go in runs of 32 at least.
+constexpr uint32_t kRouteAlone = 64;
 
 // Tokens are cut into `blocks` runs of `per_block`; each run's expert counts
 // go to the workspace ([block][pitch] u32, a pitch of whole 16 bytes; in all at
@@ -30,6 +33,7 @@ inline RoutePlan moe_route_plan(uint32_t tokens, uint32_t experts) {
     const uint32_t most = kRouteMaxBlocks * experts / route_pitch(experts);
     p.per_block = (uint32_t)div_up(tokens, most);
     p.per_block = p.per_block < 2 * kRouteWaves ? 2 * kRouteWaves : p.per_block;
+    if (tokens <= kRouteAlone) p.per_block = kRouteAlone;
     p.blocks = (uint32_t)div_up(tokens, p.per_block);
     p.bytes = p.blocks <= 1 ? 0 : (uint64_t)p.blocks * route_pitch(experts) * 4;
     return p;

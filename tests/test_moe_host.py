@@ -98,10 +98,10 @@ def test_w4_experts_refusals(change, status):
 
 def test_route_plan_bounds():
     for experts in (1, 8, 64, 1000, 1024):
-        for tokens in (0, 1, 31, 32, 33, 255, 4096, 8192, 8193, 100003, 1 << 24, (1 << 31) - 1):
+        for tokens in (0, 1, 31, 64, 65, 255, 4096, 8192, 8193, 100003, 1 << 24, (1 << 31) - 1):
             need = bsr.moe_route_ws_bytes(tokens, experts, 1)
             assert need <= 1024 * experts
-            assert (need == 0) == (tokens <= 32)
+            assert (need == 0) == (tokens <= 64)
 
 
 def test_binding_rejects_shapes_types_and_devices():
