@@ -106,11 +106,11 @@ __device__ __forceinline__ void load_logits(const void *logits, uint64_t row_at,
 }
 
 // Top-k of one row by a segment of L lanes, VPL consecutive experts each (v: this
-// lane's logits).  One lane hands slot s's id to found(s, id); lane j < top_k of
-// the segment returns slot j's weight, and whether there is one.
-template <int VPL, int L, class F>
-__device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k, bool sigmoid, bool renorm, float scale, int lane, F found,
-                                           float &weight) {
+// lane's logits); slots: top_k words of LDS of this row.  Lane j < top_k of the
+// segment returns slot j's id (-1: none) and weight.
+template <int VPL, int L>
+__device__ __forceinline__ int32_t select_row(const float (&v)[VPL], uint32_t *slots, uint32_t top_k, bool sigmoid,
+                                              bool renorm, float scale, int lane, float &weight) {
     const uint32_t sl = lane % L;  // lane within the segment
     uint32_t key[VPL], all[VPL];
     uint32_t id[VPL];
@@ -132,7 +132,7 @@ __device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k
             id[j] ^= d;
             id[j + 1] ^= d;
         }
-    uint32_t taken = 0, top = 0, slot_id = 0;  // lane j: key and id of slot j; the row's largest key
+    uint32_t taken = 0, top = 0;  // lane j: key of slot j; the row's largest key
     for (uint32_t s = 0; s < top_k; ++s) {
         const uint32_t m = segment_max<L>(key[0]);
         const uint64_t have = __ballot(m != 0 && key[0] == m);
@@ -144,13 +144,8 @@ __device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k
             won = (have >> (lane & ~(L - 1)) & ((1ull << L) - 1) & ((2ull << sl) - 1)) == 1ull << sl;
         if (s == 0) top = m;
         if (sl == s) taken = m;
-        if constexpr (L == 64) {  // one owner per wave: its id comes as a scalar, stored with all the others at the end
-            const uint32_t oid = __builtin_amdgcn_readlane(id[0], __builtin_ctzll(have));
-            if (sl == s) slot_id = oid;
-        } else if (won) {
-            found(s, id[0]);
-        }
         if (won) {
+            slots[s] = id[0];
 #pragma unroll
             for (int j = 0; j + 1 < VPL; ++j) {
                 key[j] = key[j + 1];
@@ -159,7 +154,6 @@ __device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k
             key[VPL - 1] = 0;
         }
     }
-    if (L == 64 && taken != 0) found(sl, slot_id);
     const float vmax = top != 0 ? key_logit(top) : 0.0f;
     // exp(v - vmax) with equal infinities at distance 0
     auto rel = [&](uint32_t k) {
@@ -186,7 +180,7 @@ __device__ __forceinline__ bool select_row(const float (&v)[VPL], uint32_t top_k
         total = segment_sum<L>(part);
     }
     weight = taken == 0 ? 0.0f : p / total * scale;
-    return taken != 0;
+    return taken == 0 ? -1 : (int32_t)slots[sl];
 }
 
 struct RouteShared {
@@ -194,6 +188,7 @@ struct RouteShared {
     uint32_t before[kRouteMaxExperts];              // of the blocks before this one, then the running row
     uint16_t wave_count[kRouteWaves][kRouteMaxExperts];  // of 64 slots each, then their prefix
     uint32_t wave_sums[kRouteWaves];
+    uint32_t slots[kRouteWaves][4][kRouteMaxTopK];  // ids of the rows that a wave works on
 };
 
 // total[] -> exclusive prefix over the experts; returns the sum.
@@ -284,19 +279,13 @@ __global__ __launch_bounds__(kRouteThreads) void route_select_kernel(
         for (int j = 0; j < VPL; ++j) v[j] = next[j];
         load_logits<TYPE, VPL>(logits, (uint64_t)(t + kStep) * ld, t + kStep < t1 ? e0 : experts, experts, next);
         const bool live = t < t1;
-        const uint64_t out = (uint64_t)t * top_k;
-        float w;
-        const bool any = select_row<VPL, L>(
-            v, top_k, sigmoid, renorm, scale, lane,
-            [&](uint32_t s, uint32_t id) {
-                ids[out + s] = (int32_t)id;
-                atomicAdd(&sh.total[id], 1u);  // LDS integer counts: any order gives the same
-            },
-            w);
         const uint32_t sl = lane % L;
+        float weight;
+        const int32_t id = select_row<VPL, L>(v, sh.slots[wave][lane / L], top_k, sigmoid, renorm, scale, lane, weight);
         if (live && sl < top_k) {
-            weights[out + sl] = w;
-            if (!any) ids[out + sl] = -1;
+            ids[(uint64_t)t * top_k + sl] = id;
+            weights[(uint64_t)t * top_k + sl] = weight;
+            if (id >= 0) atomicAdd(&sh.total[id], 1u);  // LDS integer counts: any order gives the same
         }
     }
     __syncthreads();
