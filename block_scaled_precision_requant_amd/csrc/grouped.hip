@@ -117,7 +117,9 @@ __global__ __launch_bounds__(256, 2) void grouped_kernel(
     const float *__restrict__ w_s, uint16_t *__restrict__ out, GroupedRows g, uint32_t N, uint32_t K,
     uint32_t tiles_n) {
     constexpr int BM = kGemmBM, BN = kGemmBN;
-    __shared__ __attribute__((aligned(1024))) char lds[TileTraits<BM, BN, 64, 64, 1, 2, false>::kLds];
+    constexpr size_t kLds = TileTraits<BM, BN, 64, 64, 1, 2, false>::kLds;
+    static_assert(TileTraits<96, BN, 96, 32, 1, 2, false>::kLds <= kLds, "the smaller tiles fit");
+    __shared__ __attribute__((aligned(1024))) char lds[kLds];
     ClassedTiles rt(g, threadIdx.x & 63);
     // (overlapping ranges could ask for more tiles than the grid has: those are not computed)
     const uint32_t tiles_m = min(rt.n0 + rt.n1 + rt.n2, gridDim.x / tiles_n);

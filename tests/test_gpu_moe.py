@@ -198,6 +198,8 @@ W4 = [  # m, n, k, group, scale type, zero points
     (1, 4096, 6144, 128, "f16", "4 bit"), (33, 65, 96, 0, "f16", None),
     # two column tiles a workgroup, the last one of 1 or 8 columns; one column, chunks cut short
     (5, 8200, 160, 32, "bf16", "any"), (16, 8193, 96, 32, "f16", None), (12, 8225, 448, 64, "f32", "4 bit"),
+    # the most LDS a workgroup takes: 16 waves of 4 rows
+    (4, 4096, 14336, 128, "bf16", None), (3, 4000, 8192, 0, "f16", "4 bit"),
     (1, 1, 1440, 32, "f32", "4 bit"), (16, 1, 288, 32, "bf16", "any"), (4, 17, 704, 64, "f16", "any")]
 
 

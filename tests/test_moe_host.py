@@ -1,6 +1,8 @@
 """Expert-layer operators on the CPU: the refusals of the C ABI and of the
 binding, the router's launch plan, and the oracle against independent forms."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -177,3 +179,15 @@ def test_oracle_products_against_dense_matmul():
         ref = sum(x[:, k] * s[j, k // 32] * ((int(wp[j, k // 2]) >> (4 * (k % 2))) % 16 - int(z[j, k // 32]))
                   for k in range(64))
         np.testing.assert_allclose(y[:, j], ref, rtol=1e-11, atol=1e-11)
+
+
+def test_launch_plans(tmp_path):
+    """The plans of the streamed kernels, the row-tile bound and the router's workspace, over sizes (host code)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "moe_plan_check")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", f"-I{root}/block_scaled_precision_requant_amd/csrc",
+                    os.path.join(root, "tests", "host", "moe_plan_check.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    cases, many, gemv = map(int, r.stdout.split()[1:])
+    assert cases > 100000 and 0 < many < cases and gemv > 100
