@@ -125,11 +125,7 @@ __global__ __launch_bounds__(256, 2) void grouped_kernel(
     const uint32_t tiles_m = min(rt.n0 + rt.n1 + rt.n2, gridDim.x / tiles_n);
     if (blockIdx.x >= tiles_m * tiles_n) return;
     uint32_t tm, tn;
-#ifdef CONTIG
-    tile_of<kGemmGroupM>(blockIdx.x, tiles_m, tiles_n, tm, tn);
-#else
     grouped_tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
-#endif
     RowTile r = rt.find(tm);
     // the same in every lane; said so, since a buffer descriptor that the compiler
     // takes for a vector costs a loop around each copy
