@@ -12,6 +12,7 @@ using bsr::check_device;
 using bsr::div_up;
 using bsr::k_ok;
 using bsr::kMaxGrid;
+using bsr::kMaxThreads;
 using bsr::launched;
 
 namespace {
@@ -38,6 +39,11 @@ int w4_check(const uint16_t *x, const uint8_t *w_packed, const void *scale, int 
 bool w4_shape_ok(int scale_type, uint32_t group, uint32_t x_rows, uint32_t k) {
     return k_ok(k) && k < bsr::kGemmTallMaxK && (uint64_t)x_rows * k < (1ull << 31) && type_ok(scale_type) &&
            (group == 0 || ((group == 32 || group == 64 || group == 128) && k % group == 0));
+}
+
+bool w4_grid_ok(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, uint32_t group, bool silu) {
+    return bsr::grouped_row_tiles(rows, experts, 16) * div_up(n, 16) <= kMaxGrid &&
+           bsr::w4_group_threads(bsr::w4_group_plan(rows, experts, silu ? n / 2 : n, k, group, silu)) <= kMaxThreads;
 }
 
 }  // namespace
@@ -86,7 +92,9 @@ int int8_grouped_gemm_blockscaled(const int8_t *a_i8, const int8_t *w_i8, const 
     if (!aligned(a_i8, 16) || !aligned(w_i8, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
         !aligned(offsets, 4) || !aligned(row_index, 4) || !aligned(out, 2))
         return BSR_EALIGN;
-    if (bsr::grouped_row_tiles(rows, experts, 16) * div_up(n, 16) > kMaxGrid) return BSR_EINVAL;
+    if (bsr::grouped_row_tiles(rows, experts, 16) * div_up(n, 16) > kMaxGrid ||
+        bsr::grouped_threads(rows, experts, n, k) > kMaxThreads)
+        return BSR_EINVAL;
     if (int st = check_device()) return st;
     return launched(bsr::launch_grouped_gemm(a_i8, w_i8, a_scale, w_scale, out,
                                              {offsets, row_index, a_rows, rows, experts}, n, k,
@@ -100,7 +108,8 @@ int moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, con
     if ((rows != 0 && !y) || !pos || !weights || !out) return BSR_ENULL;
     if (!aligned(y, 2) || !aligned(pos, 4) || !aligned(weights, 4) || !aligned(residual, 2) || !aligned(out, 2))
         return BSR_EALIGN;
-    if ((uint64_t)tokens * div_up(n, 64) > kMaxGrid) return BSR_EINVAL;
+    const uint64_t columns = (uint64_t)bsr::combine_columns(y, residual, out, n) * bsr::kCombineThreads;
+    if (tokens * div_up(n, columns) * bsr::kCombineThreads > kMaxThreads) return BSR_EINVAL;
     if (int st = check_device()) return st;
     return launched(bsr::launch_moe_combine(y, pos, weights, residual, out, tokens, top_k, rows, n,
                                             static_cast<hipStream_t>(stream)));
@@ -112,7 +121,7 @@ int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const void *sca
     if (!w4_shape_ok(scale_type, group, m, k)) return BSR_EINVAL;
     if (m == 0 || n == 0) return BSR_OK;
     if (int st = w4_check(x, w_packed, scale, scale_type, out)) return st;
-    if (div_up(m, 16) * div_up(n, 16) > kMaxGrid) return BSR_EINVAL;
+    if (!w4_grid_ok(m, 1, n, k, group, false)) return BSR_EINVAL;
     if (int st = check_device()) return st;
     return launched(bsr::launch_w4_group(x, w_packed, scale, scale_type, zero, group, out,
                                          {nullptr, nullptr, m, m, 1}, false, n, k, static_cast<hipStream_t>(stream)));
@@ -128,7 +137,7 @@ int w4a16_group_gemv_experts(const uint16_t *x, const uint8_t *w_packed, const v
     if (!offsets) return BSR_ENULL;
     if (int st = w4_check(x, w_packed, scale, scale_type, out)) return st;
     if (!aligned(offsets, 4) || !aligned(row_index, 4)) return BSR_EALIGN;
-    if (bsr::grouped_row_tiles(rows, experts, 16) * div_up(n, 16) > kMaxGrid) return BSR_EINVAL;
+    if (!w4_grid_ok(rows, experts, n, k, group, silu_mul == 1)) return BSR_EINVAL;
     if (int st = check_device()) return st;
     return launched(bsr::launch_w4_group(x, w_packed, scale, scale_type, zero, group, out,
                                          {offsets, row_index, x_rows, rows, experts}, silu_mul == 1, n, k,

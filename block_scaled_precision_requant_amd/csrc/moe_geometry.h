@@ -47,6 +47,12 @@ inline uint64_t grouped_row_tiles(uint32_t rows, uint32_t experts, uint32_t bm) 
     return (rows + used * (bm - 1)) / bm;
 }
 
+// A launch has fewer than 2^32 threads.
+constexpr uint64_t kMaxThreads = (1ull << 32) - 1;
+
+// ---- combine ----------------------------------------------------------------
+constexpr uint32_t kCombineThreads = 256;
+
 // ---- grouped GEMV (few rows per expert) -------------------------------------
 // A workgroup owns 16 output columns and a tile of up to 16 rows, or 4; its
 // waves split K in chunks of 128 bytes, two to a pass.
@@ -95,6 +101,13 @@ inline GroupedGemvPlan grouped_gemv_plan(uint32_t rows, uint32_t experts, uint32
     const uint32_t sums = p.waves * 64 * 4 * 4;
     p.lds = p.lds > sums ? p.lds : sums;
     return p;
+}
+
+// Threads of a grouped launch (its 16-row tiles below 2^31).
+inline uint64_t grouped_threads(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k) {
+    if (!grouped_gemv_rule(rows, experts, n)) return grouped_row_tiles(rows, experts, kGemmBM) * div_up(n, kGemmBN) * 256;
+    const GroupedGemvPlan p = grouped_gemv_plan(rows, experts, n, k);
+    return (uint64_t)p.row_tiles * p.col_tiles * p.waves * 64;
 }
 
 // ---- 4-bit group GEMV -------------------------------------------------------
@@ -160,5 +173,7 @@ inline W4gPlan w4_group_plan(uint32_t rows, uint32_t experts, uint32_t cols, uin
     p.lds = p.lds > sums ? p.lds : sums;
     return p;
 }
+
+inline uint64_t w4_group_threads(const W4gPlan &p) { return (uint64_t)p.row_tiles * p.col_tiles * p.waves * 64; }
 
 }  // namespace bsr

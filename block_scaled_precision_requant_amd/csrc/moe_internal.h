@@ -14,6 +14,12 @@ hipError_t launch_moe_route(const void *logits, int type, uint32_t ld, int32_t *
 hipError_t launch_moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, const uint16_t *residual,
                               uint16_t *out, uint32_t tokens, uint32_t top_k, uint32_t rows, uint32_t n,
                               hipStream_t s);
+// Columns per lane there: 8 where rows are whole 16-byte words, else 1.
+inline uint32_t combine_columns(const uint16_t *y, const uint16_t *residual, const uint16_t *out, uint32_t n) {
+    const uintptr_t any = reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(residual) |
+                          reinterpret_cast<uintptr_t>(out);
+    return n % 8 == 0 && any % 16 == 0 ? 8 : 1;
+}
 
 // Rows of a grouped call: expert e owns rows [offsets[e], offsets[e + 1]) and
 // row p reads operand row index[p] (p where index is null).  offsets null: one

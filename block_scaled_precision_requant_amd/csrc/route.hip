@@ -386,8 +386,6 @@ void launch_select(const void *logits, uint32_t ld, int32_t *ids, float *weights
 
 // ---------------------------------------------------------------- combine
 
-constexpr int kCombineThreads = 256;
-
 // V columns per lane (8: 16-byte rows; 1: any n and alignment).
 template <int V>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(
@@ -440,9 +438,7 @@ hipError_t launch_moe_route(const void *logits, int type, uint32_t ld, int32_t *
 hipError_t launch_moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, const uint16_t *residual,
                               uint16_t *out, uint32_t tokens, uint32_t top_k, uint32_t rows, uint32_t n,
                               hipStream_t s) {
-    const uintptr_t any = reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(residual) |
-                          reinterpret_cast<uintptr_t>(out);
-    if (n % 8 == 0 && any % 16 == 0) {
+    if (combine_columns(y, residual, out, n) == 8) {
         const uint32_t chunks = (uint32_t)div_up(n, 8 * kCombineThreads);
         hipLaunchKernelGGL((combine_kernel<8>), dim3(tokens * chunks), dim3(kCombineThreads), 0, s, y, pos, weights,
                            residual, out, top_k, rows, n, chunks);

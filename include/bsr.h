@@ -376,7 +376,7 @@ BSR_API int moe_route(const void *logits, int type, uint32_t ld, int32_t *ids, f
  * order follows the sizes of the call; equal calls give equal bits.
  * Limits: experts <= 65536, rows < 2^31, k < 2^24, and with row_index a_rows *
  * k < 2^32 (the rows are gathered with 32-bit offsets).
- * Errors: BSR_EINVAL (k, those limits, a_rows too small, too many workgroups),
+ * Errors: BSR_EINVAL (k, those limits, a_rows too small, a launch of 2^32 threads),
  * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  rows == 0, n == 0 or
  * experts == 0 is a valid empty problem.
  */
@@ -395,8 +395,10 @@ BSR_API int int8_grouped_gemm_blockscaled(const int8_t *a_i8, const int8_t *w_i8
  *   residual [tokens, n]     BF16 as raw u16 or NULL, 2-byte aligned
  *   out      [tokens, n]     BF16 as raw u16, 2-byte aligned; may be residual
  * Limits: 1 <= top_k <= 16.
- * Errors: BSR_EINVAL (top_k, more than 2^31 workgroups), BSR_ENULL, BSR_EALIGN,
- * BSR_EDEVICE, BSR_ELAUNCH.  rows == 0 is valid (no slot adds anything).
+ * Errors: BSR_EINVAL (top_k, a launch of 2^32 threads: one per 8 columns of a
+ * token, or per column where n % 8 != 0 or a pointer is not 16-byte aligned, in
+ * wholes of 256), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  rows == 0 is
+ * valid (no slot adds anything).
  */
 BSR_API int moe_combine(const uint16_t *y, const int32_t *pos, const float *weights, const uint16_t *residual,
                         uint16_t *out, uint32_t tokens, uint32_t top_k, uint32_t rows, uint32_t n, void *stream);
@@ -417,9 +419,8 @@ BSR_API int moe_combine(const uint16_t *y, const int32_t *pos, const float *weig
  * error of a sum is bounded with the terms |x| * scale * (32 + c + z).
  * Meant for m <= 16; every further 16 rows read the weight once more.
  * Limits: k < 2^24, m * k < 2^31 (the activations are read with 32-bit offsets).
- * Errors: BSR_EINVAL (k, group, scale_type, those limits, more than 2^31
- * workgroups),
- * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
+ * Errors: BSR_EINVAL (k, group, scale_type, those limits, a launch of 2^32
+ * threads), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
  */
 BSR_API int w4a16_group_gemv(const uint16_t *x, const uint8_t *w_packed, const void *scale, int scale_type,
                              const uint8_t *zero, uint32_t group, uint16_t *out, uint32_t m, uint32_t n, uint32_t k,

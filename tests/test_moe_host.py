@@ -88,6 +88,29 @@ def test_w4_group_refusals(change, status):
     assert _call("w4a16_group_gemv", W4, **change) == status
 
 
+# Launches end at 2^32 threads: the last sizes that pass go on to the device check.
+NODEV = bsr.BSR_EDEVICE
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the sizes that pass would be launched")
+@pytest.mark.parametrize("name, defaults, change, status", [
+    ("moe_combine", COMBINE, dict(tokens=(1 << 24) - 1, n=2048), NODEV),
+    ("moe_combine", COMBINE, dict(tokens=1 << 24, n=2048), INV),
+    ("moe_combine", COMBINE, dict(tokens=1 << 23, n=2048, y=_fake(2)), INV),
+    ("moe_combine", COMBINE, dict(tokens=1 << 24, n=1), INV),
+    ("int8_grouped_gemm_blockscaled", GROUPED, dict(rows=1 << 20, a_rows=1 << 20, experts=1, n=2047 * 128), NODEV),
+    ("int8_grouped_gemm_blockscaled", GROUPED, dict(rows=1 << 20, a_rows=1 << 20, experts=1, n=2048 * 128), INV),
+    ("int8_grouped_gemm_blockscaled", GROUPED, dict(rows=1, a_rows=1, experts=1, n=(1 << 30) - 16, k=32), NODEV),
+    ("int8_grouped_gemm_blockscaled", GROUPED, dict(rows=1, a_rows=1, experts=1, n=1 << 30, k=32), INV),
+    ("w4a16_group_gemv", W4, dict(m=1, n=(1 << 30) - 16, k=32), NODEV),
+    ("w4a16_group_gemv", W4, dict(m=1, n=1 << 30, k=32), INV),
+    ("w4a16_group_gemv_experts", W4E, dict(rows=1, n=1 << 30, k=32), INV),
+    ("w4a16_group_gemv_experts", W4E, dict(rows=1, n=1 << 30, k=32, silu_mul=1), NODEV),
+])
+def test_launch_limits(name, defaults, change, status):
+    assert _call(name, defaults, **change) == status
+
+
 @pytest.mark.parametrize("change, status", W4_BOTH + [
     (dict(rows=0), OK), (dict(experts=0), OK), (dict(rows=5), INV), (dict(experts=65537), INV), (dict(silu_mul=2), INV),
     (dict(row_index=FAKE, x_rows=0), INV),
