@@ -167,6 +167,30 @@ def test_binding_rejects_shapes_types_and_devices():
         bsr.moe_combine(z(8, 8, dt=bf), ids, wt, out)
 
 
+def test_binding_rejects_sizes_past_32_bits():
+    """Sizes the ABI's 32-bit arguments cannot hold are refused, not cut (views of one element: no memory)."""
+    big = 1 << 32
+
+    def view(*shape, dtype=torch.bfloat16):
+        return torch.zeros(1, dtype=dtype).expand(shape)
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    logits = torch.empty_strided((2, 4), (big + 4, 1), device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.moe_route(logits, *[torch.zeros(2, 2, dtype=t) for t in (i32, f32)], torch.zeros(5, dtype=i32),
+                      torch.zeros(4, dtype=i32), torch.zeros(2, 2, dtype=i32))
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.int8_grouped_gemm_blockscaled(view(1, 32, dtype=torch.int8), view(1, big + 8, 32, dtype=torch.int8),
+                                          view(1, 1, dtype=f32), view(1, big + 8, 1, dtype=f32),
+                                          torch.zeros(2, dtype=i32), view(1, big + 8))
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.moe_combine(view(1, big + 8), torch.zeros(1, 1, dtype=i32), torch.zeros(1, 1), view(1, big + 8))
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.w4a16_group_gemv(view(1, 32), view(big + 8, 16, dtype=u8), view(big + 8, 1), view(1, big + 8))
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.w4a16_group_gemv_experts(view(big + 1, 32), view(1, 8, 16, dtype=u8), view(1, 8, 1),
+                                     torch.zeros(2, dtype=i32), view(1, 8))
+
+
 def test_oracle_route_by_hand():
     inf, nan = np.inf, np.nan
     x = np.array([[1.0, 3.0, 3.0, 2.0], [-inf] * 4, [nan, -inf, 0.0, -inf], [0.0, inf, -1.0, inf]])
