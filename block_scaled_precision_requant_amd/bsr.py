@@ -310,9 +310,10 @@ def _arg(t, shape, kind, what, dev):
     return t.data_ptr()
 
 
-def _sizes(*sizes):
-    if max(sizes) > 0xFFFFFFFF:
-        raise ValueError(f"sizes and strides must fit 32 bits, got {max(sizes)}")
+def _fit(bits):
+    """Refuses sizes and strides, or-ed together, that the ABI's 32-bit arguments would cut."""
+    if bits >> 32:
+        raise ValueError("sizes and strides must fit 32 bits")
 
 
 def _same_device(t, what, dev):
@@ -355,7 +356,7 @@ def moe_route(logits, ids, weights, offsets, row_token, pos, workspace=None, sco
     if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
         raise ValueError("logits: rows with unit column stride that do not overlap")
     ld = logits.stride(0) if t > 1 else e
-    _sizes(t, e, ld)
+    _fit(t | e | ld)
     dev = logits.get_device()
     ptrs = (_arg(ids, (t, k), I32, "ids", dev), _arg(weights, (t, k), F32, "weights", dev),
             _arg(offsets, (e + 1,), I32, "offsets", dev), _arg(row_token, (t * k,), I32, "row_token", dev),
@@ -383,7 +384,7 @@ def int8_grouped_gemm_blockscaled(a_i8, w_i8, a_scale, w_scale, offsets, out, ro
     of a_i8 [A,K] / a_scale [A,K/32] times the weight w_i8 [E,N,K] / w_scale [E,N,K/32] of expert e."""
     a_rows, k = a_i8.shape
     e, n, _ = w_i8.shape
-    _sizes(a_rows, out.shape[0], e, n, k)
+    _fit(a_rows | out.shape[0] | e | n | k)
     dev = a_i8.get_device()
     a, w = _arg(a_i8, (a_rows, k), BYTES, "a_i8", dev), _arg(w_i8, (e, n, k), BYTES, "w_i8", dev)
     a_s = _arg(a_scale, (a_rows, k // 32), F32, "a_scale", dev)
@@ -397,7 +398,7 @@ def moe_combine(y, pos, weights, out, residual=None, stream=None):
     0..R-1 adds nothing)."""
     rows, n = y.shape
     t, k = pos.shape
-    _sizes(t, k, rows, n)
+    _fit(t | k | rows | n)
     dev = y.get_device()
     _launch("moe_combine", dev, stream, _arg(y, (rows, n), BF16, "y", dev), _arg(pos, (t, k), I32, "pos", dev),
             _arg(weights, (t, k), F32, "weights", dev),
@@ -412,7 +413,7 @@ def _w4_args(x, w_packed, scale, zero, dims, dev):
     if w_packed.dim() != dims:
         raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected {('two', 'three')[dims - 2]} dimensions")
     lead, n = w_packed.shape[:-2], w_packed.shape[-2]
-    _sizes(m, *lead, n, k)
+    _fit(m | w_packed.shape[0] | n | k)
     cols = scale.shape[-1]
     if cols == 0 or k % cols:
         raise ValueError(f"scale: {cols} groups do not divide K = {k}")
@@ -442,7 +443,7 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
     SiLU(gate) * up."""
     dev = x_bf16.get_device()
     ptrs, (e,), n, k = _w4_args(x_bf16, w_packed, scale, zero, 3, dev)
-    _sizes(out.shape[0], 0)
+    _fit(out.shape[0])
     off, index, o, rows = _rows_args(offsets, row_index, out, n // 2 if silu_mul else n, e, dev)
     _launch("w4a16_group_gemv_experts", dev, stream, *ptrs, off, index, 1 if silu_mul else 0, o, x_bf16.shape[0], rows,
             e, n, k)
