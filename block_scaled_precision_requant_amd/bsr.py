@@ -287,20 +287,27 @@ SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 TYPE_BF16, TYPE_F16, TYPE_F32 = 0, 1, 2
 
 
+_TYPES = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+
+
 def _type(t, what):
     """Element type of an argument that takes three: float32, float16, or BF16 (any
     other 2-byte dtype, as raw bits)."""
-    if t.dtype == torch.float32:
-        return TYPE_F32
-    if t.dtype == torch.float16:
-        return TYPE_F16
-    _kind(t, what, BF16)
-    return TYPE_BF16
+    kind = _TYPES.get(t.dtype)
+    if kind is None:
+        _kind(t, what, BF16)
+        kind = TYPE_BF16
+    return kind
 
 
 # Small decode calls last as long as the host takes to issue them, so the calls
 # below look at each tensor once and take the short ways: integers for devices
 # and pointers.
+
+# (a build of torch without devices has neither; no call reaches them there)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
 
 def _arg(t, shape, kind, what, dev):
     """Data pointer of a contiguous tensor of this shape and element kind on device `dev`."""
@@ -328,8 +335,8 @@ def _launch(name, dev, stream, *args):
     if dev < 0:
         raise ValueError("arguments must be device tensors")
     fn = getattr(_LIB or lib(), name)
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    raw = _current_stream(dev) if stream is None else stream.cuda_stream
+    if _current_device() == dev:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -406,33 +413,33 @@ def moe_combine(y, pos, weights, out, residual=None, stream=None):
             _arg(out, (t, n), BF16, "out", dev), t, k, rows, n)
 
 
-def _w4_args(x, w_packed, scale, zero, dims, dev):
-    """Pointers of (x, w_packed, scale), the scale type, the pointer of zero, the group, and (lead, n, k), of a 4-bit
-    weight w_packed [*lead, N, K/2] of `dims` dimensions for x [M, K]."""
-    m, k = x.shape
-    if w_packed.dim() != dims:
-        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected {('two', 'three')[dims - 2]} dimensions")
-    lead, n = w_packed.shape[:-2], w_packed.shape[-2]
-    _fit(m | w_packed.shape[0] | n | k)
-    cols = scale.shape[-1]
+def _w4_args(x, w_packed, scale, zero, lead, dev):
+    """Pointers of (x, w_packed, scale), the scale type, the pointer of zero, the group, and (m, n, k), of a 4-bit
+    weight w_packed [*lead, K/2] (lead: N, or E and N) for x [M, K]."""
+    m, k = x_shape = x.shape
+    groups = scale.shape
+    n, cols = lead[-1], groups[-1]
     if cols == 0 or k % cols:
         raise ValueError(f"scale: {cols} groups do not divide K = {k}")
-    kind, shape = _type(scale, "scale"), (*lead, n, cols)
-    if scale.shape != shape or not scale.is_contiguous():
-        raise ValueError(f"scale: shape {tuple(scale.shape)}, expected contiguous {shape}")
-    _same_device(scale, "scale", dev)
-    ptrs = (_arg(x, (m, k), BF16, "x_bf16", dev), _arg(w_packed, (*lead, n, k // 2), BYTES, "w_packed", dev),
+    _fit(m | lead[0] | n | k)
+    kind, shape = _type(scale, "scale"), (*lead, cols)
+    if groups != shape or not scale.is_contiguous():
+        raise ValueError(f"scale: shape {tuple(groups)}, expected contiguous {shape}")
+    if scale.get_device() != dev:
+        _same_device(scale, "scale", dev)
+    return (_arg(x, x_shape, BF16, "x_bf16", dev), _arg(w_packed, (*lead, k // 2), BYTES, "w_packed", dev),
             scale.data_ptr(), kind, None if zero is None else _arg(zero, shape, BYTES, "zero", dev),
-            0 if cols == 1 else k // cols)
-    return ptrs, lead, n, k
+            0 if cols == 1 else k // cols), m, n, k
 
 
 def w4a16_group_gemv(x_bf16, w_packed, scale, out, zero=None, stream=None):
     """out [M,N] BF16 = x_bf16 [M,K] times the 4-bit weight scale * (code - zero): w_packed [N,K/2] (low nibble
     first), scale [N,K/group] (BF16, float16 or float32; one column: one scale per row), zero [N,K/group] uint8 or
     None (8 throughout)."""
-    dev, m = x_bf16.get_device(), x_bf16.shape[0]
-    ptrs, _, n, k = _w4_args(x_bf16, w_packed, scale, zero, 2, dev)
+    if w_packed.dim() != 2:
+        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected two dimensions")
+    dev, (n, _) = x_bf16.get_device(), w_packed.shape
+    ptrs, m, n, k = _w4_args(x_bf16, w_packed, scale, zero, (n,), dev)
     _launch("w4a16_group_gemv", dev, stream, *ptrs, _arg(out, (m, n), BF16, "out", dev), m, n, k)
 
 
@@ -442,10 +449,13 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
     int8_grouped_gemm_blockscaled.  silu_mul: the first N/2 columns are gates, the others ups, and out [R,N/2] is
     SiLU(gate) * up."""
     dev = x_bf16.get_device()
-    ptrs, (e,), n, k = _w4_args(x_bf16, w_packed, scale, zero, 3, dev)
+    if w_packed.dim() != 3:
+        raise ValueError(f"w_packed: shape {tuple(w_packed.shape)}, expected three dimensions")
+    e, n, _ = w_packed.shape
+    ptrs, m, n, k = _w4_args(x_bf16, w_packed, scale, zero, (e, n), dev)
     _fit(out.shape[0])
     off, index, o, rows = _rows_args(offsets, row_index, out, n // 2 if silu_mul else n, e, dev)
-    _launch("w4a16_group_gemv_experts", dev, stream, *ptrs, off, index, 1 if silu_mul else 0, o, x_bf16.shape[0], rows,
+    _launch("w4a16_group_gemv_experts", dev, stream, *ptrs, off, index, 1 if silu_mul else 0, o, m, rows,
             e, n, k)
 
 
