@@ -7,6 +7,8 @@
 // each.  Per 32 elements two v_mfma_f32_16x16x32_bf16: P = sum x * (16 + c) and
 // X = sum x (an all-ones operand, so every column of its tile holds the row
 // sums); a group ends with acc += s * (P - (16 + z) * X), everything in FP32.
+// One scale per weight row ends every 128 elements the same way: P and X over
+// all of K, far above their difference, would round 3 to 6 times as coarsely.
 // The 16 rows of a tile are activation rows, its 16 columns weight rows.
 //
 // Bound by reading the weight once.  A workgroup owns 16 columns and its waves
@@ -221,9 +223,16 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
     const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
     uint32_t mask = 0x00780078u;  // in a register of its own: v_and_or_b32 takes one constant
     asm("" : "+v"(mask));
-    v4f psum[CT], xsum = none;  // GPC 0: over the wave's whole range
+    v4f psum[CT], xsum;
+    float row_scale[CT], row_zero[CT];  // GPC 0
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) acc[ct] = psum[ct] = none;
+    for (int ct = 0; ct < CT; ++ct) {
+        acc[ct] = none;
+        if constexpr (GPC == 0) {
+            row_scale[ct] = load_f32<STYPE>(sbase[ct], srow[ct]);
+            row_zero[ct] = p.zero != nullptr ? (float)zbase[ct][srow[ct]] : 8.0f;
+        }
+    }
     const uint8_t *xa = xs + min(c, t.rows - 1) * kPitch + 16 * q;
     // chunks [i0, i0 + XC) of a pass, whose activations are staged
     auto compute = [&](const P &b, int i0, uint32_t live) __attribute__((always_inline)) {
@@ -239,16 +248,19 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
             for (int j = 0; j < 4; ++j) {
                 const bf16x8 xv8 = *reinterpret_cast<const bf16x8 *>(xa + ii * (kW4gChunk * 2) + j * 64);
                 constexpr int per = GPC > 0 ? 4 / GPC : 4;
-                if (GPC > 0 && j % per == 0) xsum = none;
+                if (j % per == 0) xsum = none;
                 xsum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv8, ones, xsum, 0, 0, 0);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    if (GPC > 0 && j % per == 0) psum[ct] = none;
+                    if (j % per == 0) psum[ct] = none;
                     psum[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv8, codes_to_bf16((uint32_t)w[ct][j], mask),
                                                                        psum[ct], 0, 0, 0);
-                    if (GPC > 0 && j % per == per - 1) {
-                        const float s = scale_value<STYPE>(b.s[ct].bits(i * GPC + j / per));
-                        const float z = (float)b.z[ct].bits(i * GPC + j / per);
+                    if (j % per == per - 1) {
+                        float s = row_scale[ct], z = row_zero[ct];
+                        if constexpr (GPC > 0) {
+                            s = scale_value<STYPE>(b.s[ct].bits(i * GPC + j / per));
+                            z = (float)b.z[ct].bits(i * GPC + j / per);
+                        }
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             acc[ct][r] = fmaf(s, fmaf(-16.0f - z, xsum[r], psum[ct][r]), acc[ct][r]);
@@ -307,15 +319,6 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
             if (i > 0) load_x(chunk + i, true);
             store_x();
             compute(b0, i, end - chunk);
-        }
-    }
-    if constexpr (GPC == 0) {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            const float s = load_f32<STYPE>(sbase[ct], srow[ct]);
-            const float z = p.zero != nullptr ? (float)zbase[ct][srow[ct]] : 8.0f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[ct][r] = s * fmaf(-16.0f - z, xsum[r], psum[ct][r]);
         }
     }
 }

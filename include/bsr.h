@@ -414,9 +414,10 @@ BSR_API int moe_combine(const uint16_t *y, const int32_t *pos, const float *weig
  *   zero     [n, k/group] u8 zero points 0..255, or NULL: every z is 8
  *   group    32, 64 or 128 (dividing k), or 0: one scale per row of the weight
  *   out      [m, n]       BF16 as raw u16, 2-byte aligned
- * Evaluated in binary32: per group the codes enter as the exact values 16 + c
- * and (16 + z) * sum(x) is taken off, then the scale is applied once, so the
- * error of a sum is bounded with the terms |x| * scale * (32 + c + z).
+ * Evaluated in binary32: per group (group 0: per 128 elements) the codes enter
+ * as the exact values 16 + c and (16 + z) * sum(x) is taken off, then the scale
+ * is applied once, so the error of a sum is bounded with the terms |x| * scale *
+ * (32 + c + z).
  * Meant for m <= 16; every further 16 rows read the weight once more.
  * Limits: k < 2^24, m * k < 2^31 (the activations are read with 32-bit offsets).
  * Errors: BSR_EINVAL (k, group, scale_type, those limits, a launch of 2^32
