@@ -480,7 +480,7 @@ class MoeScratch:
         self.h, self.y = buf(rows, inter, dtype=bf16), buf(rows, hidden, dtype=bf16)
 
     def route(self, logits, **how):
-        """moe_route of the first len(logits) tokens; returns (rows, their buffers' views)."""
+        """moe_route of len(logits) tokens into these buffers; returns the row capacity, len(logits) * top_k."""
         t = logits.shape[0]
         if t > self.tokens:
             raise ValueError(f"{t} tokens, scratch for {self.tokens}")
@@ -490,13 +490,20 @@ class MoeScratch:
         return rows
 
 
+def _layer_tokens(x_bf16, logits):
+    t = x_bf16.shape[0]
+    if logits.shape[0] != t:  # the rows come from the logits, what they are made of from x_bf16
+        raise ValueError(f"logits: {logits.shape[0]} tokens, x_bf16 {t}")
+    return t
+
+
 def moe_prefill(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale, out, scratch, residual=None,
                 score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
     """One expert layer on int8 per-32 weights (requant_w_nvfp4_int8 of each expert): x_bf16 [T,H], router logits
     [T,E], w_gate_up [E,2I,H] (gate rows first), w_down [E,H,I] with their scales -> out [T,H] (+ residual), in six
     steps on one stream: router, activation requant, grouped gate and up, SiLU product requant, grouped down,
     weighted sum."""
-    t, inter = x_bf16.shape[0], w_down.shape[2]
+    t, inter = _layer_tokens(x_bf16, logits), w_down.shape[2]
     s = scratch
     rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
     a_i8, a_scale, gate_up, y = s.a_i8[:t], s.a_scale[:t], s.gate_up[:rows], s.y[:rows]
@@ -513,7 +520,7 @@ def moe_decode_w4(x_bf16, logits, w_gate_up, gate_up_scale, gate_up_zero, w_down
     """One expert layer on 4-bit weights with group scales, for a few tokens: as moe_prefill, with w_gate_up
     [E,2I,H/2] and w_down [E,H,I/2] packed, their scales and zero points (or None), in four steps: router, gate and up
     with the SiLU product, down, weighted sum."""
-    t = x_bf16.shape[0]
+    t = _layer_tokens(x_bf16, logits)
     s = scratch
     rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
     h, y = s.h[:rows], s.y[:rows]
