@@ -88,8 +88,8 @@ def _stream(stream, like):
 
 
 # Element kinds the kernels read and write: byte codes (int8, packed E2M1,
-# E4M3), 16-bit BF16 bits (any 2-byte dtype: torch.bfloat16, int16, uint16)
-# and binary32 scales.
+# E4M3), 16-bit BF16 bits (any 2-byte dtype: torch.bfloat16, int16, uint16; the
+# calls that read float16 as such refuse it there) and binary32 scales.
 BYTES, BF16, F32, I32 = "1-byte", "2-byte", "float32", "int32"
 _USUAL = {BYTES: {torch.int8, torch.uint8}, BF16: {torch.bfloat16, torch.int16}, F32: {torch.float32},
           I32: {torch.int32}}  # what _kind need not look at
@@ -313,6 +313,8 @@ def _arg(t, shape, kind, what, dev):
     """Data pointer of a contiguous tensor of this shape and element kind on device `dev`."""
     if t.shape != shape or t.dtype not in _USUAL[kind] or not t.is_contiguous() or t.get_device() != dev:
         _shape(t, shape, what, kind)
+        if kind == BF16 and t.dtype == torch.float16:  # a type that other arguments of these calls are read as
+            raise ValueError(f"{what}: dtype torch.float16, expected BF16 elements (torch.bfloat16, or raw bits)")
         _same_device(t, what, dev)
     return t.data_ptr()
 
@@ -490,10 +492,15 @@ class MoeScratch:
         return rows
 
 
-def _layer_tokens(x_bf16, logits):
+def _layer_tokens(x_bf16, logits, out, residual):
+    """Token count of a layer call, whose token tensors are checked before its first launch."""
     t = x_bf16.shape[0]
     if logits.shape[0] != t:  # the rows come from the logits, what they are made of from x_bf16
         raise ValueError(f"logits: {logits.shape[0]} tokens, x_bf16 {t}")
+    dev = x_bf16.get_device()
+    for v, what in ((x_bf16, "x_bf16"), (out, "out"), (residual, "residual")):
+        if v is not None:
+            _arg(v, x_bf16.shape, BF16, what, dev)
     return t
 
 
@@ -503,7 +510,7 @@ def moe_prefill(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale, ou
     [T,E], w_gate_up [E,2I,H] (gate rows first), w_down [E,H,I] with their scales -> out [T,H] (+ residual), in six
     steps on one stream: router, activation requant, grouped gate and up, SiLU product requant, grouped down,
     weighted sum."""
-    t, inter = _layer_tokens(x_bf16, logits), w_down.shape[2]
+    t, inter = _layer_tokens(x_bf16, logits, out, residual), w_down.shape[2]
     s = scratch
     rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
     a_i8, a_scale, gate_up, y = s.a_i8[:t], s.a_scale[:t], s.gate_up[:rows], s.y[:rows]
@@ -520,7 +527,7 @@ def moe_decode_w4(x_bf16, logits, w_gate_up, gate_up_scale, gate_up_zero, w_down
     """One expert layer on 4-bit weights with group scales, for a few tokens: as moe_prefill, with w_gate_up
     [E,2I,H/2] and w_down [E,H,I/2] packed, their scales and zero points (or None), in four steps: router, gate and up
     with the SiLU product, down, weighted sum."""
-    t = _layer_tokens(x_bf16, logits)
+    t = _layer_tokens(x_bf16, logits, out, residual)
     s = scratch
     rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
     h, y = s.h[:rows], s.y[:rows]

@@ -55,3 +55,45 @@ def test_layers_reject_logits_of_other_tokens(path, tokens, launched):
     with pytest.raises(ValueError, match=f"logits: {tokens} tokens, x_bf16 4"):
         getattr(layer, path)(logits=zeros(tokens, 3, dt=F32))
     assert not launched
+
+
+def _float16_calls():
+    ids, pos, off, rows = zeros(4, 2, dt=I32), zeros(4, 2, dt=I32), zeros(4, dt=I32), zeros(8, dt=I32)
+    wt, y, w4, s4 = zeros(4, 2, dt=F32), zeros(8, 64), zeros(64, 32, dt=U8), zeros(64, 2, dt=torch.float16)
+    e4, es4, x, out = zeros(3, 64, 32, dt=U8), zeros(3, 64, 2, dt=F32), zeros(4, 64), zeros(4, 64)
+    a, a_s, w, w_s = zeros(4, 64, dt=I8), zeros(4, 2, dt=F32), zeros(3, 64, 64, dt=I8), zeros(3, 64, 2, dt=F32)
+    layer = Layer()
+    return [
+        ("x_bf16", lambda h: bsr.w4a16_group_gemv(h(x), w4, s4, out)),
+        ("out", lambda h: bsr.w4a16_group_gemv(x, w4, s4, h(out))),
+        ("x_bf16", lambda h: bsr.w4a16_group_gemv_experts(h(x), e4, es4, off, out)),
+        ("out", lambda h: bsr.w4a16_group_gemv_experts(x, e4, es4, off, h(out))),
+        ("out", lambda h: bsr.int8_grouped_gemm_blockscaled(a, w, a_s, w_s, off, h(out))),
+        ("y", lambda h: bsr.moe_combine(h(y), pos, wt, out)),
+        ("residual", lambda h: bsr.moe_combine(y, pos, wt, out, residual=h(out))),
+        ("out", lambda h: bsr.moe_combine(y, pos, wt, h(out))),
+        ("x_bf16", lambda h: layer.prefill(x=h(layer.x))),
+        ("x_bf16", lambda h: layer.decode(x=h(layer.x))),
+        ("out", lambda h: layer.prefill(out=h(layer.out))),
+        ("residual", lambda h: layer.decode(residual=h(layer.out))),
+    ]
+
+
+@pytest.mark.parametrize("i", range(12))
+def test_float16_is_not_read_as_bf16(i, launched):
+    """A float16 tensor has a type of its own here (logits and scales are read as such): never raw BF16 bits."""
+    what, call = _float16_calls()[i]
+    call(lambda t: t)
+    call(lambda t: t.view(torch.int16))  # raw bits stay welcome
+    call(lambda t: t.view(torch.uint16))
+    with pytest.raises(ValueError, match=f"{what}: dtype torch.float16"):
+        call(lambda t: t.view(torch.float16))
+
+
+def test_float16_layer_inputs_are_refused_before_any_launch(launched):
+    layer = Layer()
+    for change in (dict(x=layer.x.half()), dict(out=layer.out.half()), dict(residual=layer.out.half())):
+        for path in (layer.prefill, layer.decode):
+            with pytest.raises(ValueError, match="dtype torch.float16"):
+                path(**change)
+            assert not launched
