@@ -6,6 +6,7 @@ their shapes, and a stream (default: torch's current stream on the tensors'
 device) are passed straight through.  A non-zero status raises ``BsrError``.
 There is no fallback: if libbsr.so is missing, the first call raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -331,6 +332,11 @@ def _same_device(t, what, dev):
                          f"{'the CPU' if dev < 0 else f'cuda:{dev}'}: all must be on one device")
 
 
+def _on(dev):
+    """A context in which `dev` is the current device."""
+    return contextlib.nullcontext() if dev < 0 or _current_device() == dev else torch.cuda.device(dev)
+
+
 def _launch(name, dev, stream, *args):
     """Calls an entry point with `args` and a stream (default: torch's current one on device `dev`), `dev` being
     the current device during the call."""
@@ -514,10 +520,13 @@ def moe_prefill(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale, ou
     s = scratch
     rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
     a_i8, a_scale, gate_up, y = s.a_i8[:t], s.a_scale[:t], s.gate_up[:rows], s.y[:rows]
-    requant_a_int8(x_bf16, a_i8, a_scale, stream=stream)
+    dev = x_bf16.get_device()
+    with _on(dev):  # (the two requants run on the current device)
+        requant_a_int8(x_bf16, a_i8, a_scale, stream=stream)
     int8_grouped_gemm_blockscaled(a_i8, w_gate_up, a_scale, gate_up_scale, s.offsets, gate_up,
                                   row_index=s.row_token[:rows], stream=stream)
-    silu_mul_requant_int8(gate_up[:, :inter], gate_up[:, inter:], s.h_i8[:rows], s.h_scale[:rows], stream=stream)
+    with _on(dev):
+        silu_mul_requant_int8(gate_up[:, :inter], gate_up[:, inter:], s.h_i8[:rows], s.h_scale[:rows], stream=stream)
     int8_grouped_gemm_blockscaled(s.h_i8[:rows], w_down, s.h_scale[:rows], down_scale, s.offsets, y, stream=stream)
     moe_combine(y, s.pos[:t], s.weights[:t], out, residual=residual, stream=stream)
 

@@ -97,3 +97,46 @@ def test_float16_layer_inputs_are_refused_before_any_launch(launched):
             with pytest.raises(ValueError, match="dtype torch.float16"):
                 path(**change)
             assert not launched
+
+
+class Card1(torch.Tensor):
+    """A tensor that says it is on cuda:1."""
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("path, steps", [("prefill", 6), ("decode", 4)])
+def test_layers_run_on_their_tensors_device(path, steps, monkeypatch):
+    """Every step of a layer runs with its tensors' device as the current one, whichever is current around the call."""
+    current, seen = [0], []
+
+    class device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, current[0])) or bsr.BSR_OK
+
+    monkeypatch.setattr(bsr, "_LIB", Lib())
+    monkeypatch.setattr(bsr, "_ptr", lambda t: None)
+    monkeypatch.setattr(bsr, "_stream", lambda *a: None)
+    monkeypatch.setattr(bsr, "_current_stream", lambda dev: 0)
+    monkeypatch.setattr(bsr, "_current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    layer = Layer()
+    card = lambda t: None if t is None else t.as_subclass(Card1)  # noqa: E731
+    layer.i8, layer.w4 = [card(t) for t in layer.i8], [card(t) for t in layer.w4]
+    for name, t in vars(layer.scratch).items():
+        if isinstance(t, torch.Tensor):
+            setattr(layer.scratch, name, card(t))
+    getattr(layer, path)(x=card(layer.x), logits=card(layer.logits), out=card(layer.out))
+    assert len(seen) == steps and {dev for _, dev in seen} == {1}, seen
+    assert current == [0]
