@@ -504,6 +504,7 @@ def _layer_tokens(x_bf16, logits, out, residual):
     if logits.shape[0] != t:  # the rows come from the logits, what they are made of from x_bf16
         raise ValueError(f"logits: {logits.shape[0]} tokens, x_bf16 {t}")
     dev = x_bf16.get_device()
+    _same_device(logits, "logits", dev)
     for v, what in ((x_bf16, "x_bf16"), (out, "out"), (residual, "residual")):
         if v is not None:
             _arg(v, x_bf16.shape, BF16, what, dev)

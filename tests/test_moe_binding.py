@@ -140,3 +140,12 @@ def test_layers_run_on_their_tensors_device(path, steps, monkeypatch):
     getattr(layer, path)(x=card(layer.x), logits=card(layer.logits), out=card(layer.out))
     assert len(seen) == steps and {dev for _, dev in seen} == {1}, seen
     assert current == [0]
+
+
+@pytest.mark.parametrize("path", ["prefill", "decode"])
+def test_layers_reject_logits_on_another_device(path, launched):
+    """The router would run on the logits' device and read and write the scratch there, the rest on x_bf16's."""
+    layer = Layer()
+    with pytest.raises(ValueError, match="logits: on"):
+        getattr(layer, path)(logits=layer.logits.as_subclass(Card1))
+    assert not launched
