@@ -371,7 +371,7 @@ def moe_route(logits, ids, weights, offsets, row_token, pos, workspace=None, sco
     if (e > 1 and logits.stride(1) != 1) or (t > 1 and logits.stride(0) < e):
         raise ValueError("logits: rows with unit column stride that do not overlap")
     ld = logits.stride(0) if t > 1 else e
-    _fit(t | e | ld)
+    _fit(t | e | k | ld)
     dev = logits.get_device()
     ptrs = (_arg(ids, (t, k), I32, "ids", dev), _arg(weights, (t, k), F32, "weights", dev),
             _arg(offsets, (e + 1,), I32, "offsets", dev), _arg(row_token, (t * k,), I32, "row_token", dev),

@@ -149,3 +149,11 @@ def test_layers_reject_logits_on_another_device(path, launched):
     with pytest.raises(ValueError, match="logits: on"):
         getattr(layer, path)(logits=layer.logits.as_subclass(Card1))
     assert not launched
+
+
+def test_route_top_k_past_32_bits_is_refused():
+    """Without tokens the ids [0, k] take no memory whatever k is; k = 2^32 + 2 was cut to 2."""
+    k = (1 << 32) + 2
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.moe_route(zeros(0, 4, dt=F32), zeros(0, k, dt=I32), zeros(0, k, dt=F32), zeros(5, dt=I32), zeros(0, dt=I32),
+                      zeros(0, k, dt=I32))
