@@ -435,6 +435,8 @@ def _w4_args(x, w_packed, scale, zero, lead, dev):
         raise ValueError(f"scale: shape {tuple(groups)}, expected contiguous {shape}")
     if scale.get_device() != dev:
         _same_device(scale, "scale", dev)
+    if zero is not None and zero.dtype != torch.uint8:  # numbers, not raw bytes: -1 would be read as 255
+        raise ValueError(f"zero: dtype {zero.dtype}, expected torch.uint8")
     return (_arg(x, x_shape, BF16, "x_bf16", dev), _arg(w_packed, (*lead, k // 2), BYTES, "w_packed", dev),
             scale.data_ptr(), kind, None if zero is None else _arg(zero, shape, BYTES, "zero", dev),
             0 if cols == 1 else k // cols), m, n, k

@@ -157,3 +157,17 @@ def test_route_top_k_past_32_bits_is_refused():
     with pytest.raises(ValueError, match="32 bits"):
         bsr.moe_route(zeros(0, 4, dt=F32), zeros(0, k, dt=I32), zeros(0, k, dt=F32), zeros(5, dt=I32), zeros(0, dt=I32),
                       zeros(0, k, dt=I32))
+
+
+@pytest.mark.parametrize("dtype", [torch.int8, torch.bool, torch.float8_e4m3fn])
+def test_zero_points_are_numbers_from_0_to_255(dtype, launched):
+    """The kernel reads zero points as unsigned bytes: an int8 -1 would count as 255."""
+    x, out = zeros(4, 64), zeros(4, 64)
+    w, s, z = zeros(64, 32, dt=U8), zeros(64, 2, dt=F32), zeros(64, 2, dt=U8)
+    bsr.w4a16_group_gemv(x, w, s, out, zero=z)
+    with pytest.raises(ValueError, match="zero: dtype"):
+        bsr.w4a16_group_gemv(x, w, s, out, zero=z.to(dtype))
+    e = [t.expand(3, *t.shape).contiguous() for t in (w, s, z)]
+    bsr.w4a16_group_gemv_experts(x, e[0], e[1], zeros(4, dt=I32), out, zero=e[2])
+    with pytest.raises(ValueError, match="zero: dtype"):
+        bsr.w4a16_group_gemv_experts(x, e[0], e[1], zeros(4, dt=I32), out, zero=e[2].to(dtype))
