@@ -26,9 +26,14 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// Eight codes -> BF16 16 + c, pairs (0,4) (1,5) (2,6) (3,7); mask = 0x00780078.
+// Sums are held 2^-kDown times as large: 128 elements of any finite BF16 times
+// |c - z| <= 255 then stay under binary32's largest value (255 * 128 < 2^15),
+// and powers of two change no rounding above its smallest.
+constexpr int kDown = 15;
+
+// Eight codes -> BF16 (16 + c) * 2^-kDown, pairs (0,4) (1,5) (2,6) (3,7); mask = 0x00780078.
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, uint32_t mask) {
-    constexpr uint32_t base = 0x41804180u;
+    constexpr uint32_t base = 0x41804180u - kDown * 0x00800080u;
     const v4i v = {(int)((w << 3 & mask) | base), (int)((w >> 1 & mask) | base), (int)((w >> 5 & mask) | base),
                    (int)((w >> 9 & mask) | base)};
     return __builtin_bit_cast(bf16x8, v);
@@ -127,7 +132,7 @@ struct W4Args {
     uint32_t n, k, cols, chunks_per_wave;
 };
 
-// The wave's chunks of K for one tile of t.rows <= ROWS rows: acc[ct] in MFMA
+// The wave's chunks of K for one tile of t.rows <= ROWS rows: 2^-kDown acc[ct] in MFMA
 // layout (lane: column l % 16, rows 4 * (l / 16) + r).  `xs`: this wave's LDS.
 template <int GPC, int STYPE, int CT, bool SILU, int ROWS>
 __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, const RowTile &t, uint32_t col0,
@@ -219,8 +224,8 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
     };
 
     const v4f none = {0.0f, 0.0f, 0.0f, 0.0f};
-    const v4i one4 = {0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80};
-    const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+    constexpr int kOnes = 0x3F803F80 - kDown * 0x00800080;  // 2^-kDown, twice
+    const bf16x8 ones = __builtin_bit_cast(bf16x8, v4i{kOnes, kOnes, kOnes, kOnes});
     uint32_t mask = 0x00780078u;  // in a register of its own: v_and_or_b32 takes one constant
     asm("" : "+v"(mask));
     v4f psum[CT], xsum;
@@ -356,8 +361,9 @@ __global__ __launch_bounds__(w4g_max_waves(ROWS, CT) * 64) void w4_group_kernel(
         const uint32_t col = col0 + ot * kW4gCols + (lane & 15), row = 4 * (lane >> 4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            float y = acc[ot][r];
-            if constexpr (SILU) y = y / (1.0f + expf(-y)) * acc[1][r];
+            constexpr float kUp = 1 << kDown;
+            float y = acc[ot][r] * kUp;
+            if constexpr (SILU) y = y / (1.0f + expf(-y)) * (acc[1][r] * kUp);
             if (row + r < t.rows && col < p.cols)
                 p.out[(uint64_t)(t.row0 + row + r) * p.cols + col] = f32_to_bf16_rne(y);
         }

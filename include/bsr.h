@@ -418,6 +418,8 @@ BSR_API int moe_combine(const uint16_t *y, const int32_t *pos, const float *weig
  * as the exact values 16 + c and (16 + z) * sum(x) is taken off, then the scale
  * is applied once, so the error of a sum is bounded with the terms |x| * scale *
  * (32 + c + z).
+ * No group's sum overflows for finite x.  A NaN or Inf in x leaves its own row
+ * of out unspecified, one in scale its own column (of its expert), no other.
  * Meant for m <= 16; every further 16 rows read the weight once more.
  * Limits: k < 2^24, m * k < 2^31 (the activations are read with 32-bit offsets).
  * Errors: BSR_EINVAL (k, group, scale_type, those limits, a launch of 2^32
