@@ -96,3 +96,108 @@ def test_rows_without_finite_activations_stay_among_themselves(m, group):
     for a, b in outs[1:]:
         assert np.array_equal(a[keep], outs[0][0][keep]) and np.array_equal(b[keep], outs[0][1][keep])
         assert not np.isfinite(bf16_bits_to_f64(a[1])).any()
+
+
+# ---- whole numbers: a lost block, or another group's scale, changes the bits ----
+
+def whole_case(rng, lead, m, n, k, group, zero):
+    """Activations -4 .. 4, codes 0 .. 15, scales +-2^-2 .. 1 and zero points: (x, w_packed, scale, zero, codes)."""
+    cols = 1 if group == 0 else k // group
+    x = rng.integers(1, 5, (m, k)) * rng.choice([-1, 1], (m, k))
+    codes = rng.integers(0, 16, (*lead, n, k))
+    scale = 2.0 ** rng.integers(-2, 1, (*lead, n, cols)) * rng.choice([-1, 1], (*lead, n, cols))
+    z = rng.integers(0, 256 if zero == "any" else 16, (*lead, n, cols)) if zero else None
+    return x, (codes[..., ::2] | codes[..., 1::2] << 4).astype(np.uint8), scale, z, codes
+
+
+def whole_product(x, codes, scale, z, skip=()):
+    """sum over the 32-blocks of K (but those of `skip`) of x * scale * (c - z), exact in binary32 in any order: the
+    terms are multiples of 2^-2 whose magnitudes add up to less than 2^22, as do the partial sums of the codes."""
+    k = codes.shape[-1]
+    rep = k // scale.shape[-1]
+    d = codes - (8 if z is None else np.repeat(z, rep, axis=-1))
+    keep = np.ones(k, dtype=bool)
+    for b in skip:
+        keep[32 * b:32 * b + 32] = False
+    s = np.repeat(scale, rep, axis=-1)
+    y = 0.0
+    t = 0.0
+    step = min(rep, 128)  # the kernel's unit: a group, or 128 elements of a row's scale
+    for lo in range(0, k, step):
+        part = (x[:, lo:lo + step] * keep[lo:lo + step]) @ (d[:, lo:lo + step] * s[:, lo:lo + step]).T
+        y, t = y + part, t + np.abs(part)
+    assert t.max() < 1 << 22 and np.abs(x).max() * 128 * 271 < 1 << 24
+    return y
+
+
+def bf16_rne(y):
+    f = np.ascontiguousarray(y, dtype=np.float32)
+    assert np.array_equal(f.astype(np.float64), y), "not exact in binary32"
+    u = f.view(np.uint32).astype(np.uint64)
+    return ((u + 0x7FFF + (u >> 16 & 1)) >> 16).astype(np.uint16)
+
+
+def same_values(bits, want):
+    """Equal BF16 numbers (a sum of exactly 0 may have either sign)."""
+    return np.array_equal(bf16_bits_to_f64(bits), bf16_bits_to_f64(want))
+
+
+WHOLE = [  # m, n, k, group, zero points
+    # tiles of up to 4 rows, of 16, and two column tiles a workgroup; chunks cut short, waves with one chunk and many
+    (1, 33, 32, 32, None), (3, 50, 96, 32, "any"), (4, 40, 1056, 32, "4 bit"), (2, 30, 14336, 32, "any"),
+    (1, 1000, 192, 64, "any"), (4, 64, 4160, 64, None), (3, 4000, 1024, 64, "4 bit"), (2, 50, 14336, 64, "any"),
+    (1, 20, 128, 128, "4 bit"), (4, 300, 1408, 128, "any"), (3, 70, 14336, 128, None),
+    (3, 4000, 1056, 0, "4 bit"), (2, 50, 14336, 0, "any"), (1, 130, 8192, 0, None), (4, 17, 32, 0, "any"),
+    (16, 40, 14336, 32, "any"), (5, 33, 1056, 32, None), (17, 100, 96, 32, "4 bit"), (16, 48, 14336, 64, None),
+    (9, 500, 448, 64, "any"), (16, 64, 14336, 128, "any"), (40, 30, 640, 128, "4 bit"), (16, 50, 14336, 0, "any"),
+    (7, 300, 4128, 0, None), (33, 20, 96, 0, "4 bit"), (5, 8200, 160, 32, "any"), (16, 8193, 192, 64, None),
+    (12, 8225, 384, 128, "4 bit"), (16, 8200, 288, 0, "any")]
+
+
+@pytest.mark.parametrize("m, n, k, group, zero", WHOLE)
+def test_whole_numbers(m, n, k, group, zero):
+    say("whole", m, n, k, group, zero)
+    rng = np.random.default_rng(m * 3 + n + k + group)
+    x, wp, scale, z, codes = whole_case(rng, (), m, n, k, group, zero)
+    want = bf16_rne(whole_product(x, codes, scale, z))
+    xb = torch.from_numpy(x).to(torch.bfloat16).to(DEV)
+    zt = None if z is None else to_dev(z.astype(np.uint8))
+    for kind in (torch.float32, torch.float16, torch.bfloat16):
+        out = canary_out(m, n)
+        bsr.w4a16_group_gemv(xb, to_dev(wp), torch.from_numpy(scale).to(kind).to(DEV), out, zero=zt)
+        assert same_values(host(out), want), kind
+
+
+@pytest.mark.parametrize("counts, n, k, group, zero", [
+    ([1, 0, 3], 100, 14336, 0, "any"), ([2, 1, 0, 1], 66, 14336, 64, None), ([0, 5, 1, 40], 34, 1056, 32, "any"),
+    ([16, 0, 16], 48, 14336, 128, "4 bit"), ([9, 30, 1], 2000, 416, 0, "4 bit"), ([1] * 70, 64, 384, 128, "any")])
+@pytest.mark.parametrize("gather", [False, True])
+def test_whole_numbers_by_expert(counts, n, k, group, zero, gather):
+    say("whole by expert", counts, n, k, group, zero, gather)
+    rng = np.random.default_rng(n + k + group)
+    experts, rows = len(counts), sum(counts)
+    x, wp, scale, z, codes = whole_case(rng, (experts,), rows, n, k, group, zero)
+    off = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
+    index = rng.integers(0, rows, rows).astype(np.int32) if gather else None
+    xr = x[index] if gather else x
+    args = (torch.from_numpy(x).to(torch.bfloat16).to(DEV), to_dev(wp), to_dev(scale.astype(np.float32)), to_dev(off))
+    how = dict(zero=None if z is None else to_dev(z.astype(np.uint8)), row_index=None if index is None else to_dev(index))
+    out = canary_out(rows, n)
+    bsr.w4a16_group_gemv_experts(*args, out, **how)
+    # the SiLU product of the same sums, with scales that keep the gates within the exponential's reach
+    small = 2.0 ** -9
+    pair = canary_out(rows, n // 2)
+    bsr.w4a16_group_gemv_experts(args[0], args[1], args[2] * small, args[3], pair, silu_mul=True, **how)
+    got, got_pair = host(out), bf16_bits_to_f64(host(pair))
+    for e in range(experts):
+        lo, hi = off[e], off[e + 1]
+        if lo == hi:
+            continue
+        y = whole_product(xr[lo:hi], codes[e], scale[e], None if z is None else z[e])
+        assert same_values(got[lo:hi], bf16_rne(y)), e
+        gate, up = y[:, :n // 2] * small, y[:, n // 2:] * small
+        ref = gate / (1 + np.exp(-gate)) * up
+        # gate and up are exact; the exponential is off by 2 steps of 2^-24 at most and its argument not at all, 1 + e,
+        # the quotient and the product by half a step each, the output by half a step of 2^-7, below 2^-126 (an
+        # exponential past binary32's range) by all of it
+        assert (np.abs(got_pair[lo:hi] - ref) <= (2.0 ** -8 + 8 * 2.0 ** -24) * np.abs(ref) + 2.0 ** -100).all()
