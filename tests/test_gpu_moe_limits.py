@@ -1,0 +1,126 @@
+"""The grouped products at the ends of their 32-bit offsets, and expert layers around what they must not read."""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_precision_requant_amd import bsr
+from gpu_util import DEV, canary_out, host, say
+from oracle import moe
+from oracle.compare import check_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _release_memory():
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+
+
+PAST_4_GIB = dict(experts=40, n=8192, k=16384, counts={0: 30, 38: 140, 39: 133})  # the GEMM's tiles (rows 303)
+
+
+def test_tiles_of_weights_past_4_gib():
+    """Tiles of whole and part rows whose weight and scales start past 4 GiB, on a part of their columns."""
+    experts, n, k, counts = PAST_4_GIB.values()
+    rows = sum(counts.values())
+    g = torch.Generator(DEV).manual_seed(6)
+    w = torch.randint(-127, 128, (experts, n, k), dtype=torch.int8, device=DEV, generator=g)
+    w_s = torch.rand((experts, n, k // 32), device=DEV, generator=g) * 2.0 ** -12
+    assert w.numel() > 1 << 32
+    a = torch.randint(-127, 128, (rows, k), dtype=torch.int8, device=DEV, generator=g)
+    a_s = torch.rand((rows, k // 32), device=DEV, generator=g) * 2.0 ** -8
+    c = np.zeros(experts, dtype=np.int32)
+    c[list(counts)] = list(counts.values())
+    off = np.concatenate(([0], np.cumsum(c))).astype(np.int32)
+    out = canary_out(rows, n)
+    bsr.int8_grouped_gemm_blockscaled(a, w, a_s, w_s, torch.from_numpy(off).to(DEV), out)
+    cols = torch.tensor([0, 1, 127, 128, 4095, 4096, 8063, 8064, 8191], device=DEV)
+    got = host(out[:, cols])
+    assert (host(out) != 0x7FA5).all()
+    for e in counts:
+        lo, hi = off[e], off[e + 1]
+        y, t, _ = moe.grouped(a[lo:hi].cpu().numpy(), w[e, cols][None].cpu().numpy(), a_s[lo:hi].cpu().numpy(),
+                              w_s[e, cols][None].cpu().numpy(), np.array([0, hi - lo]), None, hi - lo)
+        res = check_bf16(got[lo:hi], y, t, k)
+        say(f"expert {e}: {res}")
+        assert res.ok, str(res)
+
+
+GATHERED = [(4096, 12, 2), (4096, 400, 2), (32, 12, 2), (32, 400, 2)]  # k, rows, experts: GEMV and GEMM in turn
+GATHERED_N = 256
+
+
+@pytest.mark.parametrize("k, rows, experts", GATHERED)
+def test_gathered_operand_just_under_4_gib(k, rows, experts):
+    """The largest operand that row_index may name (a_rows * k < 2^32): its first and last rows, and rows of zeros."""
+    a_rows, n = (1 << 32) // k - 1, GATHERED_N
+    say("gathered", a_rows, k, rows)
+    g = torch.Generator(DEV).manual_seed(k + rows)
+    a = torch.empty((a_rows, k), dtype=torch.int8, device=DEV)
+    a.view(-1)[:a_rows * k // 4 * 4].view(torch.int32).random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    a_s = torch.rand((a_rows, k // 32), device=DEV, generator=g) + 0.5
+    w = torch.randint(-127, 128, (experts, n, k), dtype=torch.int8, device=DEV, generator=g)
+    w_s = torch.rand((experts, n, k // 32), device=DEV, generator=g) * 2.0 ** -12
+    rng = np.random.default_rng(rows)
+    index = rng.integers(0, a_rows, rows).astype(np.int32)
+    index[:8] = [a_rows - 1, 0, -1, a_rows, a_rows - 2, 2 ** 31 - 1, 1, -2 ** 31]
+    index[-3:] = [a_rows, a_rows - 1, 0]
+    off = np.array([0, rows // 2, rows], dtype=np.int32)
+    out = canary_out(rows, n)
+    bsr.int8_grouped_gemm_blockscaled(a, w, a_s, w_s, torch.from_numpy(off).to(DEV), out,
+                                      row_index=torch.from_numpy(index).to(DEV))
+    live = (index >= 0) & (index < a_rows)
+    at = torch.from_numpy(np.where(live, index, 0)).long().to(DEV)
+    small = np.where(live, np.arange(rows), -1).astype(np.int32)  # the same rows of a gathered copy
+    y, t, covered = moe.grouped(a[at].cpu().numpy(), w.cpu().numpy(), a_s[at].cpu().numpy(), w_s.cpu().numpy(), off,
+                                small, rows)
+    assert covered.all()
+    got = host(out)
+    res = check_bf16(got, y, t, k)
+    say(f"  {res}")
+    assert res.ok, str(res)
+    assert not (got[~live] & 0x7FFF).any()
+
+
+@pytest.mark.parametrize("tokens", [3, 300])
+@pytest.mark.parametrize("path", ["prefill", "decode"])
+def test_padded_tokens_may_hold_anything(tokens, path):
+    """Tokens without experts (a row of -inf logits) hold NaN, the scratch holds NaN, and so do the weights' scales of
+    an expert that no token takes: the other tokens keep their bits and the padded ones their residual."""
+    experts, top_k, hidden, inter, group = 6, 2, 160, 96, 32
+    g = torch.Generator(DEV).manual_seed(tokens)
+    x = torch.randn((tokens, hidden), device=DEV, generator=g).bfloat16()
+    residual = torch.randn((tokens, hidden), device=DEV, generator=g).bfloat16()
+    logits = torch.randn((tokens, experts), device=DEV, generator=g)
+    logits[:, 4] = -float("inf")                       # an expert of no token
+    padded = torch.arange(tokens, device=DEV) % 3 == 1
+    logits[padded] = -float("inf")
+
+    def weight(n, k):
+        if path == "prefill":
+            return [torch.randint(-127, 128, (experts, n, k), dtype=torch.int8, device=DEV, generator=g),
+                    torch.rand((experts, n, k // 32), device=DEV, generator=g) * 2.0 ** -10]
+        return [torch.randint(0, 256, (experts, n, k // 2), dtype=torch.uint8, device=DEV, generator=g),
+                torch.rand((experts, n, k // group), device=DEV, generator=g) * 0.02, None]
+    w13, w2 = weight(2 * inter, hidden), weight(hidden, inter)
+    run = bsr.moe_prefill if path == "prefill" else bsr.moe_decode_w4
+    got = []
+    for anything in (False, True):
+        scratch = bsr.MoeScratch(tokens, experts, top_k, hidden, inter)
+        if anything:
+            x[padded] = float("nan")
+            w13[1][4] = w2[1][4] = float("nan")
+            for b in (scratch.a_scale, scratch.gate_up, scratch.h_scale, scratch.h, scratch.y, scratch.weights):
+                b.fill_(float("nan"))
+            for b in (scratch.ids, scratch.pos, scratch.row_token, scratch.offsets):
+                b.fill_(2 ** 31 - 1)
+        out = torch.full_like(x, float("nan"))
+        run(x, logits, *w13, *w2, out, scratch, residual=residual)
+        torch.cuda.synchronize()
+        got.append(out)
+    assert torch.equal(got[0].view(torch.int16), got[1].view(torch.int16))
+    assert torch.isfinite(got[1]).all()
+    assert torch.equal(got[1][padded].view(torch.int16), residual[padded].view(torch.int16))
+    assert (got[1][~padded] != residual[~padded]).any(1).all()
