@@ -355,6 +355,7 @@ def _launch(name, dev, stream, *args):
 
 def moe_route_ws_bytes(tokens, experts, top_k):
     """Workspace bytes moe_route needs; 0 for few tokens, at most 1024 * experts."""
+    _fit(int(tokens) | int(experts) | int(top_k))
     return int(lib().moe_route_ws_bytes(int(tokens), int(experts), int(top_k)))
 
 

@@ -171,3 +171,10 @@ def test_zero_points_are_numbers_from_0_to_255(dtype, launched):
     bsr.w4a16_group_gemv_experts(x, e[0], e[1], zeros(4, dt=I32), out, zero=e[2])
     with pytest.raises(ValueError, match="zero: dtype"):
         bsr.w4a16_group_gemv_experts(x, e[0], e[1], zeros(4, dt=I32), out, zero=e[2].to(dtype))
+
+
+@pytest.mark.parametrize("sizes", [((1 << 32) + 5, 8, 2), (5, (1 << 32) + 8, 2), (5, 8, (1 << 32) + 2), (-1, 8, 2)])
+def test_workspace_of_sizes_past_32_bits_is_refused(sizes):
+    """A cut token count would name a workspace far too small."""
+    with pytest.raises(ValueError, match="32 bits"):
+        bsr.moe_route_ws_bytes(*sizes)
