@@ -305,9 +305,9 @@ BSR_API int int8_gemm_blockscaled_agroup(const int8_t *a_i8, const int8_t *w_i8,
  * int32 values in [0, rows], so no host synchronisation stands between the
  * router and the products.  It cannot be checked on the host: values outside
  * [0, rows] are clamped, a descending pair is an expert without rows, and
- * overlapping ranges leave the shared rows' outputs unspecified; no value
- * makes a kernel read or write outside its arguments.  Rows outside
- * [offsets[0], offsets[experts]) are left as they were.
+ * where the remaining ranges overlap the output of every row inside them is
+ * unspecified (some may not be written at all); no value makes a kernel read or
+ * write outside its arguments.  Rows of no range are left as they were.
  */
 
 /* Element types of the arguments that take more than one. */

@@ -124,3 +124,24 @@ def test_padded_tokens_may_hold_anything(tokens, path):
     assert torch.isfinite(got[1]).all()
     assert torch.equal(got[1][padded].view(torch.int16), residual[padded].view(torch.int16))
     assert (got[1][~padded] != residual[~padded]).any(1).all()
+
+
+@pytest.mark.parametrize("n", [72, 300])  # GEMV, GEMM
+def test_overlapping_ranges_write_no_other_rows(n):
+    """Offsets that descend and rise again ask for more tiles than there are workgroups: rows outside the ranges stay."""
+    rows, experts, k = 600, 5, 128
+    say("overlap", n)
+    g = torch.Generator(DEV).manual_seed(n)
+    a = torch.randint(-127, 128, (rows, k), dtype=torch.int8, device=DEV, generator=g)
+    w = torch.randint(-127, 128, (experts, n, k), dtype=torch.int8, device=DEV, generator=g)
+    a_s, w_s = torch.rand((rows, k // 32), device=DEV, generator=g), torch.rand((experts, n, k // 32), device=DEV, generator=g)
+    off = torch.tensor([10, 590, 10, 590, 10, 591], dtype=torch.int32, device=DEV)
+    out = canary_out(rows, n)
+    bsr.int8_grouped_gemm_blockscaled(a, w, a_s, w_s, off, out)
+    got = host(out)
+    assert (got[:10] == 0x7FA5).all() and (got[591:] == 0x7FA5).all()
+    wp = torch.randint(0, 256, (experts, n, k // 2), dtype=torch.uint8, device=DEV, generator=g)
+    out = canary_out(rows, n)
+    bsr.w4a16_group_gemv_experts(a_s[:, :1].expand(rows, k).bfloat16().contiguous(), wp, w_s, off, out)
+    got = host(out)
+    assert (got[:10] == 0x7FA5).all() and (got[591:] == 0x7FA5).all()
