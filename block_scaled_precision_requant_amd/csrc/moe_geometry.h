@@ -134,6 +134,10 @@ BSR_HD constexpr uint32_t w4g_pitch(uint32_t stage) { return stage * kW4gChunk *
 // Waves per workgroup: 16 leave a wave 128 registers, which the kernels of one
 // column tile and few rows fit.
 BSR_HD constexpr uint32_t w4g_max_waves(uint32_t rows, uint32_t ct) { return rows <= kW4gFew && ct == 1 ? 16 : 8; }
+static_assert(w4g_max_waves(kW4gFew, 1) * kW4gFew * w4g_pitch(w4g_stage(kW4gFew, 1, 0)) <= kLdsBytes &&
+                  w4g_max_waves(kW4gFew, 2) * kW4gFew * w4g_pitch(w4g_stage(kW4gFew, 2, 0)) <= kLdsBytes &&
+                  w4g_max_waves(kW4gRows, 1) * kW4gRows * w4g_pitch(w4g_stage(kW4gRows, 1, 0)) <= kLdsBytes,
+              "what the waves of a workgroup stage fits, and so do their sums (1 KB a wave and column tile)");
 
 struct W4gPlan {
     uint32_t rows;  // of a tile, at most: kW4gFew or kW4gRows

@@ -399,7 +399,6 @@ hipError_t launch_w4_group(const uint16_t *x, const uint8_t *w, const void *scal
                            uint32_t n, uint32_t k, hipStream_t s) {
     const uint32_t cols = silu ? n / 2 : n;
     const W4gPlan plan = w4_group_plan(g.rows, g.experts, cols, k, group, silu);
-    if (plan.lds > kLdsBytes) return hipErrorInvalidValue;
     const W4Args p = {x, w, scale, zero, out, n, k, cols, plan.chunks_per_wave};
     if (scale_type == 0) return launch_rows<0>(p, g, group, silu, plan, s);
     if (scale_type == 1) return launch_rows<1>(p, g, group, silu, plan, s);
