@@ -19,9 +19,10 @@ namespace bsr {
 namespace gemm_kernels {
 
 // Row tiles of kGemmBM rows in falling order of work, so that the last round of
-// workgroups is made of the small ones (181 us against 193 in the experts' order,
-// although an expert's remainder then reads its weight a second time): first those of more than
-// 64 rows (class 0), then an expert's last 33..64 rows (1), then last 1..32 (2).
+// workgroups is made of the small ones (6 % less time than in the experts' order on 6016
+// rows over 32 uneven experts, n 4096, k 2048, although an expert's remainder then reads its
+// weight a second time): first those of more than 64 rows in the experts' order (class 0),
+// then an expert's last 33..64 rows (1), then last 1..32 (2).
 struct ClassedTiles {
     GroupedRows g;
     int lane;
@@ -83,8 +84,8 @@ struct ClassedTiles {
 // consecutive tiles in turn, so that a run shares A and W rows in the XCD's L2
 // while the work of every part of the list is spread over all XCDs (one run
 // per XCD, as the dense GEMM has it, gives some XCDs the full tiles and others
-// the experts' remainders: 205 against 191 us on 6016 rows over 32 uneven
-// experts, n 4096, k 2048; runs of 64, 128 and 256 tiles level to 5 % slower).
+// the experts' remainders: 7 % slower on the 6016 rows above; runs of 64, 128
+// and 256 tiles level to 5 % slower).
 constexpr uint32_t kRun = 32;
 __device__ __forceinline__ void grouped_tile_of(uint32_t wg, uint32_t tiles_m, uint32_t tiles_n, uint32_t &tm,
                                                 uint32_t &tn) {
@@ -107,10 +108,11 @@ __device__ __forceinline__ void grouped_tile_of(uint32_t wg, uint32_t tiles_m, u
 // One tile of up to 128 x 128 outputs, four waves of 64 x 64, two workgroups
 // per CU.  An expert's last rows, when 96, 64 or 32 hold them, take a wave grid
 // that computes no more than that: each of the four waves 96 x 32, 64 x 32 or
-// 32 x 32.  MI355X: 8192 rows over 8 experts, n 28672, k 4096, 2.45-2.5 ms (770-785
-// TOPS; the dense GEMM of that size 844); 6016 rows over 32 uneven experts, n 4096, k
-// 2048, 181-186 us, where the experts' remainders cost a quarter; bound by the
-// FP32 rescale of each block as the dense GEMM is.
+// 32 x 32.  MI355X: 8192 rows over 8 experts, n 28672, k 4096, 2.49-2.54 ms (757-772
+// TOPS; the dense GEMM of that size 844), bound by the FP32 rescale of each block
+// as the dense GEMM is; 6016 rows over 32 uneven experts, n 4096, k 2048, 176-198 us by
+// their routing (510-574 TOPS), where the rest goes to the experts' remainders: tiles that
+// are part empty, stage their scales four blocks at a time and hold 32 columns a wave.
 template <bool GATHER>
 __global__ __launch_bounds__(256, 2) void grouped_kernel(
     const int8_t *__restrict__ a, const int8_t *__restrict__ w, const float *__restrict__ a_s,

@@ -11,8 +11,8 @@
 // activations and their scales of its own pass in LDS; the waves meet at the
 // end, where their FP32 sums are added in wave order.
 //
-// MI355X: one row through each of 8 experts, n 4096, k 2048 (75.6 MB) 15.5 us, 4.9 TB/s;
-// through 2 experts, n 4096, k 14336 (132 MB) 28.5 us, 4.6 TB/s; a device copy of 1 GiB
+// MI355X: one row through each of 8 experts, n 4096, k 2048 (75.6 MB) 15.5-16 us, 4.7-4.9
+// TB/s; through 2 experts, n 4096, k 14336 (132 MB) 29 us, 4.5 TB/s; a device copy of 1 GiB
 // reaches 5.1 TB/s.
 #include "moe_internal.h"
 

@@ -1,6 +1,7 @@
 // moe_geometry.h -- launch geometry and host-side plans of the expert-layer
 // kernels (router, grouped products, 4-bit group GEMV, combine).  Plain C++
-// with no HIP header, as bsr_geometry.h.
+// with no HIP header, as bsr_geometry.h.  Times at the rules: a pass in a captured
+// graph whose inputs rotate past 512 MB, so that weights come from HBM.
 #pragma once
 
 #include <stdint.h>
@@ -15,8 +16,9 @@ constexpr uint32_t kRouteMaxTopK = 16;
 constexpr uint32_t kRouteThreads = 1024;
 constexpr uint32_t kRouteWaves = kRouteThreads / 64;
 constexpr uint32_t kRouteMaxBlocks = 256;
-// One workgroup alone takes up to this many tokens (64 x 64 experts, top 8: 6.3 us,
-// in two launches 8.1; 128 x 128, top 4: 9.4 and 8.3); more go in runs of 32 at least.
+// One workgroup alone takes up to this many tokens; more go in runs of 32 at least.
+// Alone and in two launches: 64 tokens of 64 experts, top 8, 5.9 and 7.9 us, of 256
+// 11.5 and 10.3, of 1024 41.5 and 27.1; 128 tokens of 128, top 4, 9.5 and 8.1.
 constexpr uint32_t kRouteAlone = 64;
 
 // Tokens are cut into `blocks` runs of `per_block`; each run's expert counts
@@ -69,10 +71,10 @@ BSR_HD constexpr uint32_t gg_pitch() { return kGgPass * kGgChunk + 16; }
 BSR_HD constexpr uint32_t gg_wave_bytes(uint32_t rows) { return rows * (gg_pitch() + kGgPass * 4 * 4); }
 
 // The GEMV runs for one row per used expert on average, and for more while the
-// GEMM's 128 x 128 tiles would leave CUs idle.  Measured (GEMV against GEMM, us;
-// experts, n, k): 8, 4096, 14336 at 1 / 4 / 8 / 16 rows each 80 / 114 / 132 / 165 against
-// 116 / 126 / 127 / 127; 16, 512, 4096 at 1 / 16 rows 8.8 / 18.7 against 28 / 40;
-// 64, 4096, 2048 at 1 / 2 / 4 rows 67 / 91 / 113 against 71 / 84 / 109.
+// GEMM's 128 x 128 tiles would leave CUs idle.  Measured with the same rows for every
+// expert (GEMV against GEMM, us; experts, n, k): 8, 4096, 14336 at 1 / 4 / 8 / 16 rows each
+// 101 / 112 / 124 / 148 against 119 / 125 / 126 / 127; 16, 512, 4096 at 1 / 16 rows 11.5 /
+// 13.8 against 30 / 31; 64, 4096, 2048 at 1 / 2 / 4 rows 105 / 110 / 122 against 117 / 118 / 120.
 inline bool grouped_gemv_rule(uint32_t rows, uint32_t experts, uint32_t n) {
     const uint64_t used = rows < experts ? rows : experts;
     const uint64_t tiles = grouped_row_tiles(rows, experts, kGemmBM) * div_up(n, kGemmBN);
@@ -124,7 +126,8 @@ constexpr uint32_t kW4gChunk = 128;
 // hold beside the scales of a group of 32 and, from 5 rows on, the activations.
 BSR_HD constexpr uint32_t w4g_pass(uint32_t ct, uint32_t gpc) { return ct == 2 || gpc == 4 ? 2 : 4; }
 // Chunks per staging of the activations (16 rows: one, which keeps the registers
-// for the weights: 15.4 -> 14.7 us at 16 rows, N 4096, K 14336).
+// for the weights: a whole pass takes 18.1 us against 17.6 at 16 rows, N 4096, K 14336,
+// groups of 32, and 86 against 82 for 48 tokens, top 8 of 64 experts, N 4096, K 2048).
 BSR_HD constexpr uint32_t w4g_stage(uint32_t rows, uint32_t ct, uint32_t gpc) {
     return rows <= kW4gFew ? w4g_pass(ct, gpc) : 1;
 }
@@ -151,13 +154,13 @@ inline W4gPlan w4_group_plan(uint32_t rows, uint32_t experts, uint32_t cols, uin
     const uint32_t used = rows < experts ? rows : experts;
     // Tiles of 4 rows where an expert has 2 on average: a token's few rows, and
     // less to stage; the experts with more read their weight again from cache
-    // (16 tokens over 64 experts with the SiLU product 66 us, with tiles of 16 68-71).
+    // (16 tokens, top 8 of 64 experts, with the SiLU product 65-70 us, with tiles of 16 73).
     p.rows = rows <= kW4gFew || rows <= 2 * (uint64_t)used ? kW4gFew : kW4gRows;
     const uint32_t chunks = (uint32_t)div_up(k, kW4gChunk);
     p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, p.rows);
     // Two column tiles share the staged activations from 5 rows on, if that
-    // leaves every CU a workgroup (48 tokens, top 8 of 64 experts, N 4096, K 2048: 84 us
-    // against 98; at 256 tiles of 16 columns one tile each is faster, 15.5 against 20.5).
+    // leaves every CU a workgroup (48 tokens, top 8 of 64 experts, N 4096, K 2048: 82 us
+    // against 97; at 256 tiles of 16 columns one tile each is faster, 17.6 against 23.3).
     const uint64_t tiles = (uint64_t)p.row_tiles * div_up(cols, kW4gCols);
     p.ct = silu || (p.rows > kW4gFew && tiles >= 2 * (uint64_t)kGemmCus) ? 2 : 1;
     p.col_tiles = (uint32_t)div_up(cols, kW4gCols * (silu ? 1 : p.ct));

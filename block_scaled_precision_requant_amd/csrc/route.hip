@@ -13,14 +13,15 @@
 // the waves by a prefix over their counts.  Nothing depends on the order in
 // which workgroups run.  Few tokens take both steps in one workgroup.
 //
-// MI355X: one token of 64 experts 5.2 us in a graph (an empty launch 3.2); 16384 tokens
-// of 256 experts, top 8 (18.9 MB) 21 us: selection 12-14, bound by vector issue (28
-// exchanges of the sort and eight maxima per row pair), order 9, bound by the latency
-// of reading the counts.
+// MI355X: one token of 64 experts 4.9 us in a graph (an empty launch 3.2); 16384 tokens
+// of 256 experts, top 8 (18.9 MB) 21 us: selection 13-15, bound by vector issue (28
+// exchanges of the sort and eight maxima per row pair: 6240 vector instructions a SIMD,
+// 87 % of the waves' time), order 8, of which the waves wait 53 %: each of the 256
+// workgroups reads the whole table of 256 x 256 counts, 64 MB from L2 in all.
 //
 // Combine.  out[t] = residual[t] + sum over slots of weight * y[pos]: one pass
 // over the routed rows, bound by reading them once: 4099 tokens, top 8, n 4096 (301 MB)
-// 60 us, 5.0 TB/s.
+// 61 us, 5.0 TB/s (n 4095, a column per lane, 166 us).
 #include "moe_internal.h"
 
 namespace bsr {

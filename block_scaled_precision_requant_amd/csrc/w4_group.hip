@@ -19,6 +19,11 @@
 // before it is computed.  Each wave stages the activations of its own pass in
 // LDS (in the pairs' order, once per element), so the waves meet only at the
 // end, where their sums are added in wave order.
+//
+// MI355X, weights from HBM: one row, N 14336, K 4096, groups of 128 (30.8 MB) 10.5 us; 16
+// rows, N 4096, K 14336, groups of 32 (33.6 MB) 17.6 us (13.2 where the weights are in the
+// 256 MB cache): there vector issue is half of the waves' time, waiting the other half; a
+// CU takes 131 KB of weight and 459 KB of activations through its L1.
 #include "moe_internal.h"
 
 namespace bsr {
