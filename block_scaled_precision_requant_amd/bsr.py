@@ -473,7 +473,7 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
 class MoeScratch:
     """What the launches of moe_prefill and moe_decode_w4 pass between them, for up to `tokens` tokens of width
     `hidden`, `experts` experts of which a token takes `top_k`, and expert projections of width `inter`.  Calls that
-    may overlap in time need one each."""
+    may overlap in time need one each.  It holds the buffers of both calls."""
 
     def __init__(self, tokens, experts, top_k, hidden, inter, device="cuda"):
         def buf(*shape, dtype):

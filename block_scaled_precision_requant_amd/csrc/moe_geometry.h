@@ -75,6 +75,8 @@ BSR_HD constexpr uint32_t gg_wave_bytes(uint32_t rows) { return rows * (gg_pitch
 // expert (GEMV against GEMM, us; experts, n, k): 8, 4096, 14336 at 1 / 4 / 8 / 16 rows each
 // 101 / 112 / 124 / 148 against 119 / 125 / 126 / 127; 16, 512, 4096 at 1 / 16 rows 11.5 /
 // 13.8 against 30 / 31; 64, 4096, 2048 at 1 / 2 / 4 rows 105 / 110 / 122 against 117 / 118 / 120.
+// K is not looked at: small grids of a long K are left to the GEMM although the GEMV's
+// split of K suits them (8, 256, 7200 at 74 rows 25 against 100).
 inline bool grouped_gemv_rule(uint32_t rows, uint32_t experts, uint32_t n) {
     const uint64_t used = rows < experts ? rows : experts;
     const uint64_t tiles = grouped_row_tiles(rows, experts, kGemmBM) * div_up(n, kGemmBN);

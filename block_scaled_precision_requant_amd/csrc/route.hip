@@ -16,7 +16,7 @@
 // MI355X: one token of 64 experts 4.9 us in a graph (an empty launch 3.2); 16384 tokens
 // of 256 experts, top 8 (18.9 MB) 21 us: selection 13-15, bound by vector issue (28
 // exchanges of the sort and eight maxima per row pair: 6240 vector instructions a SIMD,
-// 87 % of the waves' time), order 8, of which the waves wait 53 %: each of the 256
+// 87 % of the waves' time), order 8, of which the waves wait 54 %: each of the 256
 // workgroups reads the whole table of 256 x 256 counts, 64 MB from L2 in all.
 //
 // Combine.  out[t] = residual[t] + sum over slots of weight * y[pos]: one pass
