@@ -266,10 +266,12 @@ __device__ __forceinline__ void w4_rows(const W4Args &p, const GroupedRows &g, c
                     psum[ct] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv8, codes_to_bf16((uint32_t)w[ct][j], mask),
                                                                        psum[ct], 0, 0, 0);
                     if (j % per == per - 1) {
-                        float s = row_scale[ct], z = row_zero[ct];
+                        float s, z;
                         if constexpr (GPC > 0) {
                             s = scale_value<STYPE>(b.s[ct].bits(i * GPC + j / per));
                             z = (float)b.z[ct].bits(i * GPC + j / per);
+                        } else {
+                            s = row_scale[ct], z = row_zero[ct];
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
