@@ -41,6 +41,13 @@ SIGNATURES = {
     "w4a16_group_gemv": (_int, [_vp, _vp, _vp, _int, _vp, _u32, _vp, _u32, _u32, _u32, _vp]),
     "w4a16_group_gemv_experts": (_int, [_vp, _vp, _vp, _int, _vp, _u32, _vp, _vp, _int, _vp, _u32, _u32, _u32, _u32,
                                         _u32, _vp]),
+    "quantize_w_fp8": (_int, [_vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _vp]),
+    "fp8_gemm_blockscaled": (_int, [_vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _vp]),
+    "fp8_grouped_gemm_blockscaled": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _u32, _u32, _u32, _u32, _u32,
+                                            _vp]),
+    "moe_dispatch": (_int, [_vp, _vp, _vp, _u32, _u32, _u32, _u32, _vp]),
+    "moe_dispatch_grad": (_int, [_vp, _vp, _vp, _u32, _u32, _u32, _u32, _vp]),
+    "moe_combine_grad": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _u32, _u32, _u32, _u32, _vp]),
     "bsr_status_string": (ctypes.c_char_p, [_int]),
 }
 
@@ -548,3 +555,110 @@ def moe_decode_w4(x_bf16, logits, w_gate_up, gate_up_scale, gate_up_zero, w_down
                              row_index=s.row_token[:rows], silu_mul=True, stream=stream)
     w4a16_group_gemv_experts(h, w_down, down_scale, s.offsets, y, zero=down_zero, stream=stream)
     moe_combine(y, s.pos[:t], s.weights[:t], out, residual=residual, stream=stream)
+
+
+# ---- FP8 products and rows of sorted tokens -----------------------------------
+
+_E4M3_TYPES = {torch.uint8, torch.float8_e4m3fn}
+
+
+def _e4m3(t, shape, what, dev):
+    """Data pointer of E4M3 codes: torch.float8_e4m3fn, or their bits as uint8."""
+    if t.dtype not in _E4M3_TYPES:  # another type's codes (int8, E5M2) would be read as other numbers
+        raise ValueError(f"{what}: dtype {t.dtype}, expected E4M3 codes (torch.float8_e4m3fn or uint8)")
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _shape(t, shape, what, BYTES)
+        _same_device(t, what, dev)
+    return t.data_ptr()
+
+
+def quantize_w_fp8(w_bf16, w_q, w_scale, w_qt=None, w_scale_t=None, stream=None):
+    """BF16 weight w_bf16 [N,K] (or [E,N,K], expert by expert) -> E4M3 codes w_q of its shape and float32 scales
+    w_scale [.., ceil(N/128), K/128], one per block of 128 x 128.  w_qt [.., K, N] and w_scale_t [.., K/128, N/128]
+    (both or neither; N a multiple of 128): the codes and scales transposed, the weight of the data gradient."""
+    if w_bf16.dim() not in (2, 3):
+        raise ValueError(f"w_bf16: shape {tuple(w_bf16.shape)}, expected two or three dimensions")
+    if (w_qt is None) != (w_scale_t is None):
+        raise ValueError("w_qt and w_scale_t: both or neither")
+    *lead, n, k = w_bf16.shape
+    e = lead[0] if lead else 1
+    _fit(e | n | k)
+    if k % 128 or (w_qt is not None and n % 128):
+        raise ValueError(f"w_bf16: shape {tuple(w_bf16.shape)}, K (and with w_qt N) must be multiples of 128")
+    dev = w_bf16.get_device()
+    w = _arg(w_bf16, (*lead, n, k), BF16, "w_bf16", dev)
+    q, s = _e4m3(w_q, (*lead, n, k), "w_q", dev), _arg(w_scale, (*lead, -(-n // 128), k // 128), F32, "w_scale", dev)
+    qt = None if w_qt is None else _e4m3(w_qt, (*lead, k, n), "w_qt", dev)
+    st = None if w_qt is None else _arg(w_scale_t, (*lead, k // 128, n // 128), F32, "w_scale_t", dev)
+    _launch("quantize_w_fp8", dev, stream, w, q, s, qt, st, e, n, k)
+
+
+def fp8_gemm_blockscaled(a_q, w_q, a_scale, w_scale, out, stream=None):
+    """out [M,N] BF16 = a_q [M,K] times w_q [N,K], E4M3 codes with float32 scales a_scale [M,K/128] (quantize_act with
+    group 128) and w_scale [ceil(N/128), K/128] (quantize_w_fp8)."""
+    m, k = a_q.shape
+    n, _ = w_q.shape
+    _fit(m | n | k)
+    dev = a_q.get_device()
+    _launch("fp8_gemm_blockscaled", dev, stream, _e4m3(a_q, (m, k), "a_q", dev), _e4m3(w_q, (n, k), "w_q", dev),
+            _arg(a_scale, (m, k // 128), F32, "a_scale", dev),
+            _arg(w_scale, (-(-n // 128), k // 128), F32, "w_scale", dev), _arg(out, (m, n), BF16, "out", dev), m, n, k)
+
+
+def fp8_grouped_gemm_blockscaled(a_q, w_q, a_scale, w_scale, offsets, out, row_index=None, silu_mul=False, stream=None):
+    """fp8_gemm_blockscaled grouped by expert: out[p] (BF16, rows offsets[e]..offsets[e+1]-1) = row row_index[p] (p
+    without it) of a_q [A,K] times the weight w_q [E,N,K] / w_scale [E, ceil(N/128), K/128] of expert e.  silu_mul: the
+    first N/2 columns are gates, the others ups, and out [R,N/2] is SiLU(gate) * up."""
+    a_rows, k = a_q.shape
+    e, n, _ = w_q.shape
+    _fit(a_rows | out.shape[0] | e | n | k)
+    dev = a_q.get_device()
+    a, w = _e4m3(a_q, (a_rows, k), "a_q", dev), _e4m3(w_q, (e, n, k), "w_q", dev)
+    a_s = _arg(a_scale, (a_rows, k // 128), F32, "a_scale", dev)
+    w_s = _arg(w_scale, (e, -(-n // 128), k // 128), F32, "w_scale", dev)
+    off, index, o, rows = _rows_args(offsets, row_index, out, n // 2 if silu_mul else n, e, dev)
+    _launch("fp8_grouped_gemm_blockscaled", dev, stream, a, w, a_s, w_s, off, index, 1 if silu_mul else 0, o, a_rows,
+            rows, e, n, k)
+
+
+def prefill_fp8(a_bf16, w_q, w_scale, a_q_scratch, a_scale_scratch, out, stream=None):
+    """The projection on an FP8 weight, in two launches: quantize_act (E4M3, group 128), then fp8_gemm_blockscaled."""
+    dev = a_bf16.get_device()
+    _arg(a_bf16, (out.shape[0], w_q.shape[1]), BF16, "a_bf16", dev)
+    with _on(dev):
+        quantize_act(a_bf16, a_q_scratch, a_scale_scratch, group=128, fmt=FMT_E4M3, stream=stream)
+    fp8_gemm_blockscaled(a_q_scratch, w_q, a_scale_scratch, w_scale, out, stream=stream)
+
+
+def moe_dispatch(x, pos, out, stream=None):
+    """out[pos[t,s]] = x[t]: rows of x [T,N] BF16 copied into the experts' order, out [R,N] (moe_route's pos [T,k]; one
+    outside 0..R-1 is skipped, and rows that no slot names are left as they were)."""
+    t, n = x.shape
+    rows, (_, k) = out.shape[0], pos.shape
+    _fit(t | k | rows | n)
+    dev = x.get_device()
+    _launch("moe_dispatch", dev, stream, _arg(x, (t, n), BF16, "x", dev), _arg(pos, (t, k), I32, "pos", dev),
+            _arg(out, (rows, n), BF16, "out", dev), t, k, rows, n)
+
+
+def moe_dispatch_grad(d_rows, pos, d_x, stream=None):
+    """d_x [T,N] BF16 = sum over the slots s of d_rows[pos[t,s]] (d_rows [R,N] BF16): the gradient of moe_dispatch."""
+    rows, n = d_rows.shape
+    t, k = pos.shape
+    _fit(t | k | rows | n)
+    dev = d_rows.get_device()
+    _launch("moe_dispatch_grad", dev, stream, _arg(d_rows, (rows, n), BF16, "d_rows", dev),
+            _arg(pos, (t, k), I32, "pos", dev), _arg(d_x, (t, n), BF16, "d_x", dev), t, k, rows, n)
+
+
+def moe_combine_grad(d_out, y, pos, weights, d_y, d_weights, stream=None):
+    """The gradient of moe_combine for d_out [T,N] BF16: d_y[pos[t,s]] = weights[t,s] * d_out[t] (d_y [R,N] BF16; rows
+    that no slot names are left as they were) and d_weights [T,k] float32 = the products of d_out[t] and
+    y[pos[t,s]]."""
+    rows, n = y.shape
+    t, k = pos.shape
+    _fit(t | k | rows | n)
+    dev = d_out.get_device()
+    _launch("moe_combine_grad", dev, stream, _arg(d_out, (t, n), BF16, "d_out", dev), _arg(y, (rows, n), BF16, "y", dev),
+            _arg(pos, (t, k), I32, "pos", dev), _arg(weights, (t, k), F32, "weights", dev),
+            _arg(d_y, (rows, n), BF16, "d_y", dev), _arg(d_weights, (t, k), F32, "d_weights", dev), t, k, rows, n)

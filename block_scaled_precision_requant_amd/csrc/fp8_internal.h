@@ -1,0 +1,65 @@
+// fp8_internal.h -- launchers and device helpers of the FP8 products, the weight
+// quantizer and the kernels around sorted tokens.
+#pragma once
+
+#include "fp8_geometry.h"
+#include "moe_internal.h"
+
+namespace bsr {
+
+// Operands of an FP8 product (no validation: the C-ABI layer has checked every
+// argument).  offsets null in `rows`: dense, one weight for all rows.
+struct Fp8Args {
+    const uint8_t *a, *w;
+    const float *a_s, *w_s;
+    uint16_t *out;
+    GroupedRows rows;
+    uint32_t n, k;
+    bool silu;
+};
+
+hipError_t launch_fp8_gemm(const Fp8Args &p, hipStream_t s);
+hipError_t launch_fp8_stream(const Fp8Args &p, const Fp8StreamPlan &plan, hipStream_t s);
+hipError_t launch_quantize_w_fp8(const uint16_t *w, uint8_t *q, float *scale, uint8_t *qt, float *scale_t,
+                                 uint32_t experts, uint32_t n, uint32_t k, hipStream_t s);
+hipError_t launch_moe_dispatch(const uint16_t *x, const int32_t *pos, uint16_t *out, uint32_t tokens, uint32_t top_k,
+                               uint32_t rows, uint32_t n, hipStream_t s);
+hipError_t launch_moe_dispatch_grad(const uint16_t *d_rows, const int32_t *pos, uint16_t *d_x, uint32_t tokens,
+                                    uint32_t top_k, uint32_t rows, uint32_t n, hipStream_t s);
+hipError_t launch_moe_combine_grad(const uint16_t *d_out, const uint16_t *y, const int32_t *pos, const float *weights,
+                                   uint16_t *d_y, float *d_weights, uint32_t tokens, uint32_t top_k, uint32_t rows,
+                                   uint32_t n, hipStream_t s);
+
+#ifdef __HIPCC__
+typedef int v8i __attribute__((ext_vector_type(8)));
+
+// BF16 nearest to x, ties to even, and NaN for NaN (v_cvt_pk_bf16_f32).
+__device__ __forceinline__ uint16_t f32_to_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+// Sixteen rows of E4M3 codes times sixteen others over one block of 128: lane l holds
+// 32 codes of row l % 16 of `w` and of `a`, the same elements of the block for both;
+// its result is out(a row l % 16, w row 4 * (l / 16) + r), in binary32.  (Scale
+// operands of 0 select the instruction without block exponents.)
+__device__ __forceinline__ v4f fp8_dot16(v8i w, v8i a) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, v4f{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+
+// gate / (1 + exp(-gate)) * up; for gate below -88 the quotient is -0.
+__device__ __forceinline__ float silu_product(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
+// Four columns of one output row, those below n.  `wide`: out and n keep 8-byte words whole.
+__device__ __forceinline__ void store4(uint16_t *out, uint64_t row, uint32_t col, uint32_t n, v4f v, bool wide) {
+    uint16_t *p = out + row * n + col;
+    if (wide) {
+        if (col < n)
+            *reinterpret_cast<ushort4 *>(p) =
+                make_ushort4(f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3]));
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (col + r < n) p[r] = f32_to_bf16(v[r]);
+}
+#endif
+
+}  // namespace bsr

@@ -447,6 +447,127 @@ BSR_API int w4a16_group_gemv_experts(const uint16_t *x, const uint8_t *w_packed,
                                      const int32_t *row_index, int silu_mul, uint16_t *out, uint32_t x_rows,
                                      uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, void *stream);
 
+/* ---- FP8 products and rows of sorted tokens ---------------------------------
+ *
+ * E4M3 codes with F32 scales per 128: activations per (row, 128 elements), as
+ * quantize_act writes them (group 128, BSR_FMT_E4M3: the FP8 activation of page
+ * "metrale_model_layers/layers/ops/fp8_moe_grouped_tc_w8a8.rs"), weights per block
+ * of 128 rows x 128 elements, as quantize_w_fp8 writes them.  Since the blocks are
+ * square, the transposed codes with the transposed scales are a weight of the same
+ * form: the data gradient of a product is the same product on them.
+ */
+
+/*
+ * Weight quantizer: BF16 -> E4M3 codes and one scale per block of 128 x 128.
+ *   w_bf16    [experts, n, k]               BF16 as raw u16, 16-byte aligned
+ *   w_q       [experts, n, k]               u8 E4M3 codes, 16-byte aligned
+ *   w_scale   [experts, ceil(n/128), k/128] f32, 4-byte aligned
+ *   w_qt      [experts, k, n]               u8, the codes transposed, 16-byte
+ *             aligned, or NULL; then n % 128 == 0
+ *   w_scale_t [experts, k/128, n/128]       f32, w_scale transposed, 4-byte
+ *             aligned; NULL if and only if w_qt is
+ * Per block (the last block of rows may be shorter): s = fl32(amax / 448); s == 0
+ * gives scale +0 and codes 0, else the E4M3 code nearest fl32(v / s), ties to the
+ * even code, at most 448 in magnitude.
+ * Errors: BSR_EINVAL (k == 0, k % 128 != 0, n % 128 != 0 with w_qt, a launch of 2^32
+ * threads: 256 per block), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
+ * experts == 0 or n == 0 is a valid empty problem.
+ */
+BSR_API int quantize_w_fp8(const uint16_t *w_bf16, uint8_t *w_q, float *w_scale, uint8_t *w_qt, float *w_scale_t,
+                           uint32_t experts, uint32_t n, uint32_t k, void *stream);
+
+/*
+ * FP8 product: out[i, j] = bf16_rne( FP32 sum over blocks b of 128 elements of
+ * fl32(a_scale[i, b] * w_scale[j / 128, b]) * P[i, j, b] ), P the dot product of
+ * block b by the FP8 matrix core.
+ *   a_q     [m, k]               u8 E4M3 codes, 16-byte aligned
+ *   w_q     [n, k]               u8 E4M3 codes, 16-byte aligned
+ *   a_scale [m, k/128]           f32, 4-byte aligned
+ *   w_scale [ceil(n/128), k/128] f32, 4-byte aligned
+ *   out     [m, n]               BF16 as raw u16, 2-byte aligned
+ * The matrix core adds the products of 8 consecutive codes in fixed point, each cut
+ * below 2^-13 of the largest one's power of two (a code stands for its value to 2^-4,
+ * so what is cut is below 1/64 of what the largest code leaves open), and the groups of
+ * 8 in binary32.  The result is within 4e-3 relative or 1 BF16 ulp of the FP64 value,
+ * or where that is larger within 7 * 2^-13 of the sum over the groups of their largest
+ * scaled product, plus the worst-case FP32 error of the sum.  The order of the sum
+ * follows the sizes of the call; equal calls give equal bits.  A NaN code, and a
+ * scale of NaN or Inf, makes only its own row (a_q, a_scale), column (w_q) or 128
+ * columns (w_scale) of out other than finite.
+ * Limits: k < 2^23, m and n < 2^31.
+ * Errors: BSR_EINVAL (k == 0, k % 128 != 0, those limits, a launch of 2^32 threads),
+ * BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  m == 0 or n == 0 is a valid empty
+ * problem.
+ */
+BSR_API int fp8_gemm_blockscaled(const uint8_t *a_q, const uint8_t *w_q, const float *a_scale, const float *w_scale,
+                                 uint16_t *out, uint32_t m, uint32_t n, uint32_t k, void *stream);
+
+/*
+ * fp8_gemm_blockscaled grouped by expert, ragged row counts: row p of expert e is
+ * operand row row_index[p] (p where row_index is NULL) times the weight of e.
+ *   a_q     [a_rows, k]                   a_scale [a_rows, k/128]
+ *   w_q     [experts, n, k]               w_scale [experts, ceil(n/128), k/128]
+ *   offsets, row_index as int8_grouped_gemm_blockscaled
+ *   silu_mul 0: out [rows, n].  1: columns 0..n/2-1 of the weight are the gate and
+ *           n/2..n-1 the up projection, out [rows, n/2] = bf16_rne( fl32(gate /
+ *           fl32(1 + exp(-gate))) * up ), gate and up in binary32; n % 256 == 0
+ * Limits: experts <= 65536, rows and n < 2^31, k < 2^23, and with row_index a_rows *
+ * k < 2^32 (the rows are gathered with 32-bit offsets).
+ * Errors: as fp8_gemm_blockscaled; BSR_EINVAL too for a_rows too small (NULL
+ * row_index needs a_rows >= rows, row_index a_rows >= 1), silu_mul other than 0 or 1,
+ * n % 256 != 0 with it, and those limits.  rows == 0, n == 0 or experts == 0 is a
+ * valid empty problem.
+ */
+BSR_API int fp8_grouped_gemm_blockscaled(const uint8_t *a_q, const uint8_t *w_q, const float *a_scale,
+                                         const float *w_scale, const int32_t *offsets, const int32_t *row_index,
+                                         int silu_mul, uint16_t *out, uint32_t a_rows, uint32_t rows, uint32_t experts,
+                                         uint32_t n, uint32_t k, void *stream);
+
+/*
+ * Rows of tokens copied into the experts' order: out[pos[t, s]] = x[t] for every
+ * slot s, for products that take no row_index.  A slot whose pos is outside [0,
+ * rows) is skipped; rows of out that no slot names are left as they were.  Where two
+ * slots of different tokens name one row (moe_route's pos has no such pair) each
+ * element of it is one of theirs.
+ *   x   [tokens, n]     BF16 as raw u16, 2-byte aligned
+ *   pos [tokens, top_k] i32, 4-byte aligned
+ *   out [rows, n]       BF16 as raw u16, 2-byte aligned
+ * Limits: 1 <= top_k <= 16, n < 2^31.
+ * Errors: BSR_EINVAL (those limits, a launch of 2^32 threads: 256 per 2048 columns of
+ * a token, or per slot if those are more), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  tokens == 0,
+ * n == 0 or rows == 0 is a valid empty problem.
+ */
+BSR_API int moe_dispatch(const uint16_t *x, const int32_t *pos, uint16_t *out, uint32_t tokens, uint32_t top_k,
+                         uint32_t rows, uint32_t n, void *stream);
+
+/*
+ * Gradient of moe_dispatch: d_x[t] = bf16_rne( sum over slots s of d_rows[pos[t, s]]
+ * ), in binary32, the slots in order; a slot whose pos is outside [0, rows) adds
+ * nothing and reads nothing (a token without slots gets 0).
+ *   d_rows [rows, n], d_x [tokens, n]  BF16 as raw u16, 2-byte aligned
+ * Other arguments, limits and errors as moe_dispatch; rows == 0 gives zeros.
+ */
+BSR_API int moe_dispatch_grad(const uint16_t *d_rows, const int32_t *pos, uint16_t *d_x, uint32_t tokens,
+                              uint32_t top_k, uint32_t rows, uint32_t n, void *stream);
+
+/*
+ * Gradient of moe_combine for d_out = dL/d out (that of its residual is d_out):
+ * with p = pos[t, s],
+ *   d_y[p] = bf16_rne( weights[t, s] * d_out[t] ),
+ *   d_weights[t, s] = sum over j of d_out[t, j] * y[p, j], in binary32.
+ * A slot whose p is outside [0, rows) has d_weights 0 and touches no row; rows of d_y
+ * that no slot names are left as they were.  Where several slots name one row
+ * (moe_route's pos has no such pair) each element of it is one of theirs, not the
+ * sum.  The order of a sum follows n; equal calls give equal bits.
+ *   d_out   [tokens, n]     BF16 as raw u16, 2-byte aligned
+ *   y, d_y  [rows, n]       BF16 as raw u16, 2-byte aligned; d_y may be y
+ *   pos     [tokens, top_k] i32, weights, d_weights [tokens, top_k] f32, 4-byte aligned
+ * Limits and errors as moe_dispatch.  n == 0 and rows == 0 give d_weights of 0.
+ */
+BSR_API int moe_combine_grad(const uint16_t *d_out, const uint16_t *y, const int32_t *pos, const float *weights,
+                             uint16_t *d_y, float *d_weights, uint32_t tokens, uint32_t top_k, uint32_t rows,
+                             uint32_t n, void *stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 BSR_API const char *bsr_status_string(int status);
 

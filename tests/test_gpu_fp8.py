@@ -1,0 +1,240 @@
+"""FP8 products on the GPU against the 64-bit oracle: dense and grouped by expert, the
+SiLU product, values that are not finite, offsets outside the rows, whole numbers bit
+for bit."""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_precision_requant_amd import bsr
+from gpu_util import CANARY, DEV, canary_out, host, largest_products, say, to_dev
+from oracle import fp8, moe
+from oracle.compare import bf16_bits_to_f64, bf16_ulp, check_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+def codes(rng, *shape):
+    """E4M3 codes over all finite values."""
+    c = rng.integers(0, 127, shape).astype(np.uint8)
+    return c | (rng.integers(0, 2, shape).astype(np.uint8) << 7)
+
+
+def scales(rng, *shape):
+    return (rng.uniform(0.5, 2.0, shape) * 2.0 ** rng.integers(-12, -4, shape)).astype(np.float32)
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+def product(a, w):
+    """(y, T) of operands given as values, T so that fp8.terms of its steps bound the error: with the matrix core's cut."""
+    y, t = fp8.product(a, w)
+    return y, t + fp8.CUT * 2.0 ** 24 / (fp8.terms(a.shape[1]) + 2) * largest_products(a, w)
+
+
+def run_dense(a, w, a_s, w_s):
+    m, n = len(a), len(w)
+    # (the rows around the output show what is written outside it)
+    around = canary_out(m + 2, n)
+    out = around[1:m + 1]
+    bsr.fp8_gemm_blockscaled(to_dev(a), to_dev(w), to_dev(a_s), to_dev(w_s), out)
+    got = host(around)
+    assert (got[0] == CANARY).all() and (got[-1] == CANARY).all()
+    return got[1:-1].view(np.uint16)
+
+
+DENSE = [  # one row to many, one block to past 64 of them, columns off every tile
+    (1, 1, 128), (1, 128, 128), (1, 4096, 256), (2, 130, 14336), (3, 33, 256), (16, 64, 384), (17, 257, 640), (32, 48, 1152),
+    (33, 96, 1152), (63, 640, 128), (64, 200, 1024), (65, 129, 256), (100, 300, 512), (128, 128, 8320), (129, 257, 384),
+    (255, 1000, 512), (300, 130, 16640), (1000, 77, 256), (512, 4096, 256), (1025, 513, 384), (4100, 4360, 384)]
+
+
+@pytest.mark.parametrize("m, n, k", DENSE)
+def test_dense(m, n, k):
+    say("fp8", m, n, k)
+    rng = np.random.default_rng(m * 7919 + n * 31 + k)
+    a, w = codes(rng, m, k), codes(rng, n, k)
+    a_s, w_s = scales(rng, m, k // 128), scales(rng, blocks(n), k // 128)
+    got = run_dense(a, w, a_s, w_s)
+    y, t = product(fp8.values_a(a, a_s), fp8.values_w(w, w_s))
+    res = check_bf16(got, y, t, k, fp8.terms(k))
+    say(f"  {res}")
+    assert res.ok, str(res)
+    assert np.array_equal(got, run_dense(a, w, a_s, w_s)), "equal calls give equal bits"
+
+
+@pytest.mark.parametrize("m, n, k", [(1, 160, 512), (16, 33, 1280), (64, 128, 256), (130, 130, 1280), (2100, 8300, 256)])
+def test_dense_whole_numbers(m, n, k):
+    """Small whole codes and scales of powers of two: every partial sum is exact, so the result is the BF16 nearest to
+    it, bit for bit -- a block, row or column that is left out or taken twice shows at once."""
+    say("fp8 whole", m, n, k)
+    rng = np.random.default_rng(m + n + k)
+    small = fp8.e4m3_nearest(np.arange(-4.0, 5.0))
+    a, w = small[rng.integers(0, 9, (m, k))], small[rng.integers(0, 9, (n, k))]
+    a_s = (2.0 ** rng.integers(-2, 3, (m, k // 128))).astype(np.float32)
+    w_s = (2.0 ** rng.integers(-2, 3, (blocks(n), k // 128))).astype(np.float32)
+    y, _ = fp8.product(fp8.values_a(a, a_s), fp8.values_w(w, w_s))
+    want = torch.from_numpy(y.astype(np.float32)).bfloat16().view(torch.int16).numpy().view(np.uint16)
+    got = run_dense(a, w, a_s, w_s)
+    assert np.array_equal(got & 0x7FFF | (got & 0x8000) * (got & 0x7FFF != 0),
+                          want & 0x7FFF | (want & 0x8000) * (want & 0x7FFF != 0))
+
+
+@pytest.mark.parametrize("m, n, k", [(3, 200, 384), (40, 300, 512), (300, 400, 384), (2100, 8300, 256)])
+def test_not_finite_stays_in_its_place(m, n, k):
+    say("fp8 nan", m, n, k)
+    rng = np.random.default_rng(5)
+    a, w = codes(rng, m, k), codes(rng, n, k)
+    a_s, w_s = scales(rng, m, k // 128), scales(rng, blocks(n), k // 128)
+    clean = run_dense(a, w, a_s, w_s)
+    bad_row, bad_col, bad_block = m - 2, n // 2, blocks(n) - 1
+    a[bad_row, k - 1] = 0x7F
+    a_s[0, 1] = np.inf
+    w[bad_col, 5] = 0xFF
+    w_s[bad_block, 0] = np.nan
+    got = run_dense(a, w, a_s, w_s)
+    touched = np.zeros((m, n), dtype=bool)
+    touched[[0, bad_row]] = True
+    touched[:, bad_col] = True
+    touched[:, 128 * bad_block:] = True
+    assert np.array_equal(got[~touched], clean[~touched])
+    assert not np.isfinite(bf16_bits_to_f64(got[:, bad_col])).any()
+    assert not np.isfinite(bf16_bits_to_f64(got[[0, bad_row]])).any()
+    assert not np.isfinite(bf16_bits_to_f64(got[:, 128 * bad_block:])).any()
+
+
+def test_out_of_any_alignment_and_views():
+    """An output two bytes off, operands inside larger buffers, float8 tensors."""
+    rng = np.random.default_rng(9)
+    for m, n, k in ((5, 64, 256), (150, 260, 256)):
+        a, w = codes(rng, m + 1, k), codes(rng, n + 3, k)
+        a_s, w_s = scales(rng, m + 1, k // 128), scales(rng, blocks(n), k // 128)
+        flat = canary_out(1, m * n + 2)[0]
+        out = flat[1:-1].view(m, n)
+        bsr.fp8_gemm_blockscaled(to_dev(a)[1:].view(torch.float8_e4m3fn), to_dev(w)[2:-1], to_dev(a_s)[1:], to_dev(w_s), out)
+        y, t = product(fp8.values_a(a[1:], a_s[1:]), fp8.values_w(w[2:-1], w_s))
+        res = check_bf16(host(out).view(np.uint16), y, t, k, fp8.terms(k))
+        assert res.ok, str(res)
+        assert int(flat[0]) == CANARY and int(flat[-1]) == CANARY
+
+
+# ---- grouped ------------------------------------------------------------------
+
+def counts(kind, experts, rows, rng):
+    """Rows of each expert: `rows` in all, or fewer."""
+    if kind == "even":
+        return np.full(experts, rows // experts)
+    if kind == "one":
+        c = np.zeros(experts, dtype=int)
+        c[experts // 2] = rows
+        return c
+    cuts = np.sort(rng.integers(0, rows + 1, experts - 1)) if experts > 1 else np.array([], dtype=int)
+    c = np.diff(np.concatenate(([0], cuts, [rows])))
+    if kind == "holes":
+        c[rng.random(experts) < 0.4] = 0
+    return c
+
+
+def run_grouped(a, w, a_s, w_s, offsets, index, rows, silu):
+    n = w.shape[1]
+    out = canary_out(rows, n // 2 if silu else n)
+    bsr.fp8_grouped_gemm_blockscaled(to_dev(a), to_dev(w), to_dev(a_s), to_dev(w_s), to_dev(offsets.astype(np.int32)), out,
+                                     row_index=None if index is None else to_dev(index.astype(np.int32)), silu_mul=silu)
+    return host(out).view(np.uint16)
+
+
+def check_grouped(got, a, w, a_s, w_s, offsets, index, rows, silu, k):
+    y, t, covered = fp8.grouped(fp8.values_a(a, a_s), w, w_s, offsets, index, rows, product)
+    assert (got[~covered] == CANARY).all(), "a row outside the offsets was written"
+    if not covered.any():
+        return
+    if not silu:
+        res = check_bf16(got[covered], y[covered], t[covered], k, fp8.terms(k))
+        say(f"  {res}")
+        assert res.ok, str(res)
+        return
+    want, bound = moe.silu_mul(y[covered], t[covered], fp8.terms(k))
+    out = bf16_bits_to_f64(got[covered])
+    err = np.abs(out - want)
+    # the nearest BF16 is half a step away, a step where the bound crosses a power of two
+    assert (err <= bound + bf16_ulp(np.abs(want) + bound) + 2.0 ** -133).all(), np.max(err - bound)
+
+
+GROUPED = [  # rows, experts, n, k, counts
+    (1, 1, 256, 128, "even"), (1, 4, 40, 128, "one"), (8, 64, 256, 256, "random"), (15, 3, 33, 384, "random"),
+    (16, 1, 256, 128, "even"), (17, 1, 130, 256, "even"), (40, 5, 64, 512, "holes"), (64, 2, 768, 1024, "random"),
+    (100, 3, 129, 384, "random"), (130, 4, 256, 2176, "one"), (200, 200, 48, 256, "even"), (300, 6, 512, 512, "holes"),
+    (515, 2, 384, 768, "random"), (1000, 8, 256, 256, "random"), (1100, 3, 300, 384, "one"), (2600, 4, 768, 384, "random"),
+    (700, 2, 4096, 256, "random"), (5000, 70, 130, 128, "holes"), (5000, 3, 5120, 256, "random")]
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("rows, experts, n, k, kind", GROUPED)
+def test_grouped(rows, experts, n, k, kind, gather, silu):
+    if silu and n % 256:
+        n = 256 * blocks(n)
+    say("fp8 grouped", rows, experts, n, k, kind, gather, silu)
+    rng = np.random.default_rng(rows * 101 + experts * 7 + n + k)
+    a_rows = max(1, rows // 3) if gather else rows
+    a, w = codes(rng, a_rows, k), codes(rng, experts, n, k)
+    # (gates of a few units, so that the SiLU's bend is inside)
+    a_s, w_s = scales(rng, a_rows, k // 128), scales(rng, experts, blocks(n), k // 128)
+    a_s *= np.float32(2.0 ** -7)
+    offsets = np.concatenate(([0], np.cumsum(counts(kind, experts, rows, rng))))
+    index = None
+    if gather:
+        index = rng.integers(0, a_rows, rows)
+        index[rng.random(rows) < 0.1] = -1
+        index[rng.random(rows) < 0.05] = a_rows
+    got = run_grouped(a, w, a_s, w_s, offsets, index, rows, silu)
+    check_grouped(got, a, w, a_s, w_s, offsets, index, rows, silu, k)
+
+
+@pytest.mark.parametrize("offsets", [
+    [0, 0, 0, 0, 0], [5, 5, 9, 9, 12], [-3, 4, 4, 100, 7], [40, 3, 3, 2, 1], [0, 300, 300, 300, 300], [2, 290, 1, 1, 1],
+    [-(2 ** 31), 2 ** 31 - 1, 0, 0, 0]])
+@pytest.mark.parametrize("rows", [12, 300])
+def test_offsets_outside_the_rows(offsets, rows):
+    say("fp8 offsets", offsets, rows)
+    rng = np.random.default_rng(rows)
+    n, k = 160, 256
+    a, w = codes(rng, rows, k), codes(rng, 4, n, k)
+    a_s, w_s = scales(rng, rows, 2), scales(rng, 4, 2, 2)
+    got = run_grouped(a, w, a_s, w_s, np.array(offsets), None, rows, False)
+    check_grouped(got, a, w, a_s, w_s, np.array(offsets), None, rows, False, k)
+
+
+@pytest.mark.parametrize("shape", [(4, 128, 128), (16, 384, 256)])
+def test_data_gradient_on_the_transposed_weight(shape):
+    """d_x = d_y @ W on the transposed codes and scales is the product with W's own values."""
+    experts, n, k = shape
+    rng = np.random.default_rng(3)
+    w_bf = torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).bfloat16().to(DEV)
+    new = lambda *s, dt=torch.uint8: torch.empty(s, dtype=dt, device=DEV)  # noqa: E731
+    q, qt = new(experts, n, k), new(experts, k, n)
+    s, st = new(experts, n // 128, k // 128, dt=torch.float32), new(experts, k // 128, n // 128, dt=torch.float32)
+    bsr.quantize_w_fp8(w_bf, q, s, w_qt=qt, w_scale_t=st)
+    rows = 50
+    d, d_s = codes(rng, rows, n), scales(rng, rows, n // 128)
+    offsets = np.concatenate(([0], np.cumsum(counts("random", experts, rows, rng))))
+    out = canary_out(rows, k)
+    bsr.fp8_grouped_gemm_blockscaled(to_dev(d), qt, to_dev(d_s), st, to_dev(offsets.astype(np.int32)), out)
+    got = host(out).view(np.uint16)
+    d64, qh, sh = fp8.values_a(d, d_s), q.cpu().numpy(), s.cpu().numpy()
+    for e in range(experts):
+        lo, hi = offsets[e], offsets[e + 1]
+        if lo < hi:
+            v = fp8.values_w(qh[e], sh[e])
+            res = check_bf16(got[lo:hi], *product(d64[lo:hi], np.ascontiguousarray(v.T)), n, fp8.terms(n))
+            assert res.ok, str(res)
+
+
+def test_dense_equals_one_expert():
+    rng = np.random.default_rng(11)
+    for m, n, k in ((7, 256, 384), (600, 512, 256)):
+        a, w = codes(rng, m, k), codes(rng, 1, n, k)
+        a_s, w_s = scales(rng, m, k // 128), scales(rng, 1, n // 128, k // 128)
+        one = run_grouped(a, w, a_s, w_s, np.array([0, m]), None, m, False)
+        check_grouped(one, a, w, a_s, w_s, np.array([0, m]), None, m, False, k)

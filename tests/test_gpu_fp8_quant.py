@@ -1,0 +1,91 @@
+"""The weight quantizer on the GPU against the oracle, bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_precision_requant_amd import bsr
+from gpu_util import DEV, host, say, to_dev
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+
+def bits(x):
+    return torch.from_numpy(np.asarray(x, dtype=np.float32)).bfloat16()
+
+
+def check(w, transposed):
+    """w [E, N, K] BF16 tensor."""
+    e, n, k = w.shape
+    b = -(-n // 128)
+    fill = lambda *s: torch.full(s, 0xA5, dtype=torch.uint8, device=DEV)  # noqa: E731
+    q, s = fill(e * n * k + 32), torch.full((e * b * (k // 128) + 2,), -7.0, device=DEV)
+    qv, sv = q[16:-16].view(e, n, k), s[1:-1].view(e, b, k // 128)
+    qt = st = None
+    if transposed:
+        qt, st = fill(e, k, n), torch.full((e, k // 128, n // 128), -7.0, device=DEV)
+    bsr.quantize_w_fp8(w.to(DEV), qv, sv, w_qt=qt, w_scale_t=st)
+    got_q, got_s = host(qv), host(sv)
+    assert (host(q)[:16] == 0xA5).all() and (host(q)[-16:] == 0xA5).all() and float(s[0]) == float(s[-1]) == -7.0
+    for i in range(e):
+        want_q, want_s = fp8.quantize_w(w[i].float().numpy())
+        assert np.array_equal(got_s[i].view(np.uint32), want_s.view(np.uint32))
+        assert np.array_equal(got_q[i], want_q)
+    if transposed:
+        assert np.array_equal(host(qt), got_q.transpose(0, 2, 1)) and np.array_equal(host(st), got_s.transpose(0, 2, 1))
+
+
+@pytest.mark.parametrize("e, n, k, transposed", [
+    (1, 1, 128, False), (1, 7, 256, False), (1, 127, 128, False), (1, 128, 128, True), (1, 129, 384, False), (3, 200, 128, False),
+    (2, 256, 384, True), (5, 128, 640, True), (1, 1000, 2048, False), (1, 1152, 1280, True)])
+def test_random(e, n, k, transposed):
+    say("quantize_w_fp8", e, n, k, transposed)
+    g = torch.Generator().manual_seed(n + k)
+    w = torch.randn(e, n, k, generator=g) * torch.exp2(torch.randint(-20, 20, (e, n, 1), generator=g).float())
+    check(w.bfloat16(), transposed)
+
+
+def test_values():
+    """Zero blocks, one value a block, signed zeros, the largest and smallest BF16, quotients between two codes."""
+    w = torch.zeros(1, 128, 128 * 8)
+    w[0, :, 128:256] = -0.0
+    w[0, 5, 256 + 9] = -3.0
+    w[0, :, 384:512] = torch.randint(-255, 256, (128, 128), generator=torch.Generator().manual_seed(1)).float()
+    w[0, 0, 512], w[0, 1, 513] = 3.3895313892515355e38, -1e38
+    w[0, 3, 640], w[0, 4, 641], w[0, 9, 642] = 9.2e-41, 1e-39, -2e-40       # subnormals: a scale of few bits
+    w[0, 0, 768] = 448.0                                                    # scale 1: the grid and its midpoints
+    grid = torch.from_numpy(fp8.E4M3[:127].astype(np.float32))
+    mid = (grid[1:] + grid[:-1]) / 2
+    w[0, 1, 768:768 + 127], w[0, 2, 768:768 + 126], w[0, 3, 768:768 + 126] = grid, mid, -mid
+    w[0, 7, 896] = 1.5 * 2.0 ** -126                                        # the smallest normals
+    check(w.bfloat16(), True)
+
+
+def test_two_dimensions_and_float8():
+    w = torch.randn(256, 384, generator=torch.Generator().manual_seed(2)).bfloat16()
+    q = torch.empty(256, 384, dtype=torch.float8_e4m3fn, device=DEV)
+    s = torch.empty(2, 3, device=DEV)
+    bsr.quantize_w_fp8(w.to(DEV), q, s)
+    want_q, want_s = fp8.quantize_w(w.float().numpy())
+    assert np.array_equal(host(q.view(torch.uint8)), want_q) and np.array_equal(host(s), want_s)
+    # and what it stands for is the weight, to half a step of the codes
+    back = q.float() * s.repeat_interleave(128, 0).repeat_interleave(128, 1)
+    top = s.repeat_interleave(128, 0).repeat_interleave(128, 1)
+    err, ref = (back.cpu() - w.float()).abs(), w.float().abs()
+    # 2^-4 of the value, or half of the subnormal step; the quotient's and the scale's own roundings
+    assert (err <= ref * (2.0 ** -4 + 2.0 ** -22) + top.cpu() * 2.0 ** -10 * (1 + 2.0 ** -22)).all()
+
+
+def test_past_4_gib():
+    """Codes and BF16 weight past 4 GiB of elements' offsets: the last expert is as it is alone."""
+    e, n, k = 9, 16384, 16384
+    last = torch.randn(n, k, generator=torch.Generator(DEV).manual_seed(4), device=DEV).bfloat16()
+    w = torch.zeros(e, n, k, dtype=torch.bfloat16, device=DEV)
+    w[-1] = last
+    q = torch.full((e, n, k), 0xA5, dtype=torch.uint8, device=DEV)
+    s = torch.empty(e, n // 128, k // 128, device=DEV)
+    bsr.quantize_w_fp8(w, q, s)
+    q1, s1 = torch.empty(n, k, dtype=torch.uint8, device=DEV), torch.empty(n // 128, k // 128, device=DEV)
+    bsr.quantize_w_fp8(last, q1, s1)
+    assert torch.equal(q[-1], q1) and torch.equal(s[-1], s1)
+    assert not q[:-1].any() and not s[:-1].any()
