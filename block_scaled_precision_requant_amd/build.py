@@ -19,8 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsr.so")
 SOURCES = ["requant.hip", "gemm.hip", "gemv.hip", "w4a16.hip", "route.hip", "grouped.hip", "grouped_gemv.hip",
-           "w4_group.hip", "fp8_gemm.hip", "fp8_stream.hip", "fp8_quant.hip", "moe_tokens.hip", "api.hip", "api_moe.hip",
-           "api_fp8.hip"]
+           "w4_group.hip", "fp8_gemm.hip", "fp8_tiles_few.hip", "fp8_tiles_64.hip", "fp8_tiles_128.hip",
+           "fp8_tiles_256.hip", "fp8_stream.hip", "fp8_quant.hip", "moe_tokens.hip", "api.hip", "api_moe.hip", "api_fp8.hip"]
 # The streaming-read kernel bench.py reports as bandwidth context: a library of
 # its own, so libbsr.so exports only the entry points include/bsr.h declares.
 READ_LIB = os.path.join(PKG, "libbsr_read.so")

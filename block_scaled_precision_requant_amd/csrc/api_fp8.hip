@@ -27,7 +27,7 @@ int product_check(const void *a_q, const void *w_q, const float *a_scale, const 
 }
 
 int product(const bsr::Fp8Args &p, void *stream) {
-    if (bsr::fp8_choice(p.rows.rows, p.rows.experts, p.n, p.k, p.silu, p.rows.offsets != nullptr).threads > kMaxThreads)
+    if (bsr::fp8_choice(p.rows.rows, p.rows.experts, p.n, p.k, p.silu).threads > kMaxThreads)
         return BSR_EINVAL;
     if (int st = check_device()) return st;
     return launched(bsr::launch_fp8_gemm(p, static_cast<hipStream_t>(stream)));

@@ -11,32 +11,46 @@
 namespace bsr {
 
 constexpr uint32_t kFp8Block = 128;       // elements of a scale block, and a stage of K
-constexpr uint32_t kFp8MaxK = 1u << 23;   // 256 rows are addressed with 32-bit offsets
+constexpr uint32_t kFp8MaxK = 1u << 23;   // the rows of a tile are addressed with 32-bit offsets
 
 inline bool fp8_k_ok(uint32_t k) { return k != 0 && k % kFp8Block == 0 && k < kFp8MaxK; }
 
 // ---- product, tiles through LDS ---------------------------------------------
-// 256 x 256 outputs by eight waves of 128 x 64, or 128 x 128 by four of 64 x 64.
-constexpr uint32_t kFp8Tall = 256;
-constexpr uint32_t kFp8Tile = 128;
+// Shapes of a workgroup's tile, in the order of kFp8Shapes.  `cost`: tenths of a
+// microsecond that one round of workgroups on every CU takes at k = 4096 (MI355X, the
+// weight in the cache behind the L2); `last`: the same where a last round leaves half of
+// the places empty.
+struct Fp8Shape {
+    uint16_t bm, bn, threads, per_cu, cost, last;
+};
+constexpr uint32_t kFp8NumShapes = 16;
+constexpr Fp8Shape kFp8Shapes[kFp8NumShapes] = {
+    {16, 16, 256, 2, 71, 65},     {16, 32, 256, 1, 70, 70},    {16, 64, 256, 1, 87, 87},    {16, 128, 256, 1, 142, 142},
+    {32, 16, 256, 1, 66, 66},     {32, 32, 256, 1, 72, 72},    {32, 64, 256, 1, 102, 102},  {32, 128, 192, 1, 158, 158},
+    {64, 16, 256, 1, 71, 71},     {64, 32, 256, 1, 84, 84},    {64, 64, 256, 1, 116, 116},  {64, 128, 256, 1, 170, 170},
+    {128, 64, 512, 1, 160, 160},  {128, 128, 512, 1, 243, 243}, {256, 128, 512, 1, 404, 404}, {256, 256, 512, 1, 530, 530},
+};
+// Two workgroups of 128 x 128 by four waves a CU, where there are tiles for more than a
+// round of every larger shape: an entry of its own, since the tile is the same.
+constexpr Fp8Shape kFp8Pair = {128, 128, 256, 2, 405, 245};
+constexpr uint32_t kFp8PairIndex = kFp8NumShapes;
+BSR_HD constexpr Fp8Shape fp8_shape(uint32_t i) { return i == kFp8PairIndex ? kFp8Pair : kFp8Shapes[i]; }
 
-// ---- product, operands streamed into registers --------------------------------
-// A workgroup owns 16 mt rows by 16 ct columns; its waves split K in chunks of
-// 128, kFp8Pass of them in flight.
-constexpr uint32_t kFp8Pass = 2;
+// ---- product, the weight streamed into registers ------------------------------
+// A workgroup owns 16 rows by 16 ct columns; its waves split K in chunks of 128, two of
+// them in flight.
 constexpr uint32_t kFp8MaxWaves = 8;
+constexpr uint32_t kFp8Few = 4;  // rows (of an expert, on average) up to which it runs
 
 struct Fp8StreamPlan {
-    uint32_t mt, ct, row_tiles, col_tiles, waves, chunks_per_wave, lds;
+    uint32_t ct, row_tiles, col_tiles, waves, chunks_per_wave, lds;
 };
 
-inline Fp8StreamPlan fp8_stream_plan(uint32_t rows, uint32_t experts, uint32_t cols, uint32_t k, bool silu, uint32_t mt,
-                                     uint32_t ct) {
+inline Fp8StreamPlan fp8_stream_plan(uint32_t rows, uint32_t experts, uint32_t cols, uint32_t k, bool silu) {
     Fp8StreamPlan p;
-    p.mt = mt;
-    p.ct = ct;
-    p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, 16 * mt);
-    p.col_tiles = (uint32_t)div_up(cols, 16 * (silu ? ct / 2 : ct));
+    p.ct = silu ? 2 : 1;
+    p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, 16);
+    p.col_tiles = (uint32_t)div_up(cols, 16);
     const uint32_t chunks = k / kFp8Block;
     uint64_t waves = 2 * kFp8MaxWaves * (uint64_t)kGemmCus / ((uint64_t)p.row_tiles * p.col_tiles);
     waves = waves > 1 ? waves : 1;
@@ -44,31 +58,57 @@ inline Fp8StreamPlan fp8_stream_plan(uint32_t rows, uint32_t experts, uint32_t c
     waves = waves < chunks ? waves : chunks;
     p.chunks_per_wave = (uint32_t)div_up(chunks, waves);
     p.waves = (uint32_t)div_up(chunks, p.chunks_per_wave);
-    p.lds = p.waves * mt * ct * 64 * 16;
+    p.lds = p.waves * p.ct * 64 * 16;
     return p;
 }
 
-// Which kernel a product runs: streamed (plan) or tiles of `bm` x `bm`.
+// Which kernel a product runs: streamed (plan), or tiles of shape `shape`.
 struct Fp8Choice {
     bool stream;
     Fp8StreamPlan plan;
-    uint32_t bm, tiles_m, tiles_n;
+    uint32_t shape, tiles_m, tiles_n;
     uint64_t threads;
 };
 
-inline Fp8Choice fp8_choice(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool silu, bool grouped) {
+// The weight alone is read for up to kFp8Few rows (1 / 4 / 8 rows, n 28672, k 4096:
+// streamed 23.6 / 24.4 / 28.1 us, in tiles 27.8 / 28.1 / 28.1).  Else the shape whose
+// rounds cost least: one round on all CUs if any shape has one, so that for few rows the
+// columns, for many the tile's area, are what grows.  Measured against its neighbours
+// (us; rows, n, k; the chosen shape first): 64, 4096, 14336: 64 x 16 18.0, 64 x 32 20.4;
+// 256, 4096, 4096: 64 x 64 11.6, 128 x 64 13.9, 64 x 32 14.9; 512, 4096, 14336: 128 x 64
+// 43.6, 64 x 128 51, 128 x 128 58; 128, 28672, 8192: 128 x 128 62, 64 x 128 72; 1024,
+// 14336, 4096: 256 x 256 63, pairs 77; 2048, 4096, 14336: 256 x 128 129, pairs 143.
+// Experts' rows are not known here: their tiles are counted as if each expert that can
+// have rows left half a tile empty.
+inline Fp8Choice fp8_choice(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool silu) {
     Fp8Choice c = {};
-    c.stream = rows <= 64 || rows <= 16 * (uint64_t)experts;
+    const uint64_t used = rows < experts ? rows : experts;
+    c.stream = rows <= kFp8Few * used;
     if (c.stream) {
-        const uint32_t tiles = grouped ? 1 : (uint32_t)div_up(rows, 16);
-        c.plan = fp8_stream_plan(rows, experts, silu ? n / 2 : n, k, silu, tiles > 2 ? 4 : tiles, silu || tiles > 1 ? 2 : 1);
+        c.plan = fp8_stream_plan(rows, experts, silu ? n / 2 : n, k, silu);
         c.threads = (uint64_t)c.plan.row_tiles * c.plan.col_tiles * c.plan.waves * 64;
         return c;
     }
-    c.bm = grouped_row_tiles(rows, experts, kFp8Tall) * div_up(n, kFp8Tall) >= kGemmCus ? kFp8Tall : kFp8Tile;
-    c.tiles_m = (uint32_t)grouped_row_tiles(rows, experts, c.bm);
-    c.tiles_n = (uint32_t)div_up(n, c.bm);
-    c.threads = (uint64_t)c.tiles_m * c.tiles_n * (c.bm == kFp8Tall ? 512 : 256);
+    uint64_t best = ~0ull;
+    for (uint32_t i = 0; i <= kFp8PairIndex; ++i) {
+        const Fp8Shape f = fp8_shape(i);
+        if (silu && f.bn == 16) continue;
+        uint64_t tiles_m = div_up(rows, f.bm);
+        if (experts > 1) {
+            tiles_m = (2 * (uint64_t)rows + used * f.bm) / (2 * f.bm);
+            tiles_m = tiles_m > used ? tiles_m : used;
+        }
+        const uint64_t tiles = tiles_m * div_up(n, f.bn), slots = (uint64_t)f.per_cu * kGemmCus, left = tiles % slots;
+        const uint64_t cost = tiles / slots * f.cost + (left == 0 ? 0 : (2 * left <= slots ? f.last : f.cost));
+        if (cost <= best) {  // (of equal ones the larger tile)
+            best = cost;
+            c.shape = i;
+        }
+    }
+    const Fp8Shape f = fp8_shape(c.shape);
+    c.tiles_m = (uint32_t)grouped_row_tiles(rows, experts, f.bm);
+    c.tiles_n = (uint32_t)div_up(n, f.bn);
+    c.threads = (uint64_t)c.tiles_m * c.tiles_n * f.threads;
     return c;
 }
 

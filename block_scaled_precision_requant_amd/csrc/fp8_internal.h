@@ -20,6 +20,10 @@ struct Fp8Args {
 
 hipError_t launch_fp8_gemm(const Fp8Args &p, hipStream_t s);
 hipError_t launch_fp8_stream(const Fp8Args &p, const Fp8StreamPlan &plan, hipStream_t s);
+hipError_t launch_fp8_tiles_few(const Fp8Args &p, const Fp8Choice &c, hipStream_t s);
+hipError_t launch_fp8_tiles_64(const Fp8Args &p, const Fp8Choice &c, hipStream_t s);
+hipError_t launch_fp8_tiles_128(const Fp8Args &p, const Fp8Choice &c, hipStream_t s);
+hipError_t launch_fp8_tiles_256(const Fp8Args &p, const Fp8Choice &c, hipStream_t s);
 hipError_t launch_quantize_w_fp8(const uint16_t *w, uint8_t *q, float *scale, uint8_t *qt, float *scale_t,
                                  uint32_t experts, uint32_t n, uint32_t k, hipStream_t s);
 hipError_t launch_moe_dispatch(const uint16_t *x, const int32_t *pos, uint16_t *out, uint32_t tokens, uint32_t top_k,

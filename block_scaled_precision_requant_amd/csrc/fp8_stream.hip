@@ -179,19 +179,8 @@ void launch_stream(const Fp8Args &p, const Fp8StreamPlan &plan, bool wide, hipSt
 hipError_t launch_fp8_stream(const Fp8Args &p, const Fp8StreamPlan &plan, hipStream_t s) {
     const uint32_t cols = p.silu ? p.n / 2 : p.n;
     const bool wide = cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 8 == 0;
-#define BSR_STREAM(M, C, P)                                       \
-    if (plan.mt == M && plan.ct == C) {                        \
-        if (p.silu) {                                          \
-            if constexpr (C % 2 == 0) launch_stream<M, C, P, true>(p, plan, wide, s); \
-        } else {                                               \
-            launch_stream<M, C, P, false>(p, plan, wide, s);      \
-        }                                                      \
-    }
-    BSR_STREAM(1, 1, 2)
-    BSR_STREAM(1, 2, 2)
-    BSR_STREAM(2, 2, 2)
-    BSR_STREAM(4, 2, 1)
-#undef BSR_STREAM
+    if (p.silu) launch_stream<1, 2, 2, true>(p, plan, wide, s);
+    else launch_stream<1, 1, 2, false>(p, plan, wide, s);
     return hipGetLastError();
 }
 

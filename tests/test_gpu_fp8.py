@@ -45,12 +45,16 @@ def run_dense(a, w, a_s, w_s):
 
 
 DENSE = [  # one row to many, one block to past 64 of them, columns off every tile
-    (1, 1, 128), (1, 128, 128), (1, 4096, 256), (2, 130, 14336), (3, 33, 256), (16, 64, 384), (17, 257, 640), (32, 48, 1152),
-    (33, 96, 1152), (63, 640, 128), (64, 200, 1024), (65, 129, 256), (100, 300, 512), (128, 128, 8320), (129, 257, 384),
-    (255, 1000, 512), (300, 130, 16640), (1000, 77, 256), (512, 4096, 256), (1025, 513, 384), (4100, 4360, 384)]
+    (1, 1, 128), (1, 128, 128), (1, 4096, 256), (2, 130, 14336), (3, 33, 256), (4, 65, 8320), (5, 40, 128), (16, 64, 384),
+    (17, 257, 640), (32, 48, 1152), (33, 96, 1152), (63, 640, 128), (64, 200, 1024), (65, 129, 256), (100, 300, 512),
+    (128, 128, 8320), (129, 257, 384), (255, 1000, 512), (300, 130, 16640), (1000, 77, 256), (1025, 513, 384)]
+SHAPES = [  # one size for each shape of tile, a few rows and columns short of whole ones (test_fp8_choices.py)
+    (13, 4090, 640), (15, 8190, 384), (9, 16380, 640), (16, 28670, 128), (30, 4090, 640), (27, 8188, 384), (32, 16381, 640),
+    (31, 28671, 256), (61, 4090, 640), (127, 4093, 384), (255, 4091, 640), (63, 28669, 256), (510, 4090, 384),
+    (1021, 4093, 640), (2045, 4089, 384), (4091, 4090, 640), (2501, 8190, 256)]
 
 
-@pytest.mark.parametrize("m, n, k", DENSE)
+@pytest.mark.parametrize("m, n, k", DENSE + SHAPES)
 def test_dense(m, n, k):
     say("fp8", m, n, k)
     rng = np.random.default_rng(m * 7919 + n * 31 + k)
@@ -64,7 +68,7 @@ def test_dense(m, n, k):
     assert np.array_equal(got, run_dense(a, w, a_s, w_s)), "equal calls give equal bits"
 
 
-@pytest.mark.parametrize("m, n, k", [(1, 160, 512), (16, 33, 1280), (64, 128, 256), (130, 130, 1280), (2100, 8300, 256)])
+@pytest.mark.parametrize("m, n, k", [(1, 160, 512), (16, 33, 1280), (64, 128, 256), (130, 130, 1280), (40, 300, 8448)] + SHAPES)
 def test_dense_whole_numbers(m, n, k):
     """Small whole codes and scales of powers of two: every partial sum is exact, so the result is the BF16 nearest to
     it, bit for bit -- a block, row or column that is left out or taken twice shows at once."""
@@ -81,7 +85,7 @@ def test_dense_whole_numbers(m, n, k):
                           want & 0x7FFF | (want & 0x8000) * (want & 0x7FFF != 0))
 
 
-@pytest.mark.parametrize("m, n, k", [(3, 200, 384), (40, 300, 512), (300, 400, 384), (2100, 8300, 256)])
+@pytest.mark.parametrize("m, n, k", [(3, 200, 384), (40, 300, 512), (300, 400, 384)] + [(m, n, 384) for m, n, _ in SHAPES])
 def test_not_finite_stays_in_its_place(m, n, k):
     say("fp8 nan", m, n, k)
     rng = np.random.default_rng(5)
@@ -167,6 +171,7 @@ GROUPED = [  # rows, experts, n, k, counts
     (100, 3, 129, 384, "random"), (130, 4, 256, 2176, "one"), (200, 200, 48, 256, "even"), (300, 6, 512, 512, "holes"),
     (515, 2, 384, 768, "random"), (1000, 8, 256, 256, "random"), (1100, 3, 300, 384, "one"), (2600, 4, 768, 384, "random"),
     (700, 2, 4096, 256, "random"), (5000, 70, 130, 128, "holes"), (5000, 3, 5120, 256, "random")]
+GROUPED += [(m, 1, 256 * (n // 256 + 1), k, "even") for m, n, k in SHAPES] + [(m, 3, n, k, "random") for m, n, k in SHAPES[4:]]
 
 
 @pytest.mark.parametrize("silu", [False, True])
