@@ -70,6 +70,22 @@ struct Fp8Choice {
     uint64_t threads;
 };
 
+// Rounds of workgroups that shape i takes for `tiles` tiles, by their cost.
+inline uint64_t fp8_cost(uint32_t i, uint64_t tiles) {
+    const Fp8Shape f = fp8_shape(i);
+    const uint64_t slots = (uint64_t)f.per_cu * kGemmCus, left = tiles % slots;
+    return tiles / slots * f.cost + (left == 0 ? 0 : (2 * left <= slots ? f.last : f.cost));
+}
+
+// Row tiles of shape i that `rows` rows of `used` experts make, as far as the host can
+// say: each expert leaves half a tile empty.
+inline uint64_t fp8_expected_tiles(uint32_t i, uint32_t rows, uint64_t used) {
+    const uint32_t bm = fp8_shape(i).bm;
+    if (used == 1) return div_up(rows, bm);
+    const uint64_t tiles = (2 * (uint64_t)rows + used * bm) / (2 * bm);
+    return tiles > used ? tiles : used;
+}
+
 // The weight alone is read for up to kFp8Few rows (1 / 4 / 8 rows, n 28672, k 4096:
 // streamed 23.6 / 24.4 / 28.1 us, in tiles 27.8 / 28.1 / 28.1).  Else the shape whose
 // rounds cost least: one round on all CUs if any shape has one, so that for few rows the
@@ -78,8 +94,14 @@ struct Fp8Choice {
 // 256, 4096, 4096: 64 x 64 11.6, 128 x 64 13.9, 64 x 32 14.9; 512, 4096, 14336: 128 x 64
 // 43.6, 64 x 128 51, 128 x 128 58; 128, 28672, 8192: 128 x 128 62, 64 x 128 72; 1024,
 // 14336, 4096: 256 x 256 63, pairs 77; 2048, 4096, 14336: 256 x 128 129, pairs 143.
-// Experts' rows are not known here: their tiles are counted as if each expert that can
-// have rows left half a tile empty.
+// Several experts with tiles for most of the CUs go by their rows on average, since
+// reading the weights is most of the time and wide tiles read them best: 64 x 128 below
+// 32 (64 experts of 8, n 4096, k 2048: 105 us, streamed 167, 32 x 128 126), 256 x 128
+// below 96 or while 256 x 256 has less than two rounds (6016 rows over 32 uneven experts, n
+// 2048, k 4096: 105, 256 x 256 119, 128 x 128 123, 64 x 128 122), else 256 x 256 (64 of 128,
+// n 4096, k 2048: 158, 256 x 128 171).
+// (128 x 64, whose two groups copy little each, is left to one weight: 3234 rows of 64
+// experts, n 256, k 7808: 55 us against 46 of 64 x 128.)
 inline Fp8Choice fp8_choice(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool silu) {
     Fp8Choice c = {};
     const uint64_t used = rows < experts ? rows : experts;
@@ -89,20 +111,23 @@ inline Fp8Choice fp8_choice(uint32_t rows, uint32_t experts, uint32_t n, uint32_
         c.threads = (uint64_t)c.plan.row_tiles * c.plan.col_tiles * c.plan.waves * 64;
         return c;
     }
-    uint64_t best = ~0ull;
-    for (uint32_t i = 0; i <= kFp8PairIndex; ++i) {
-        const Fp8Shape f = fp8_shape(i);
-        if (silu && f.bn == 16) continue;
-        uint64_t tiles_m = div_up(rows, f.bm);
-        if (experts > 1) {
-            tiles_m = (2 * (uint64_t)rows + used * f.bm) / (2 * f.bm);
-            tiles_m = tiles_m > used ? tiles_m : used;
-        }
-        const uint64_t tiles = tiles_m * div_up(n, f.bn), slots = (uint64_t)f.per_cu * kGemmCus, left = tiles % slots;
-        const uint64_t cost = tiles / slots * f.cost + (left == 0 ? 0 : (2 * left <= slots ? f.last : f.cost));
-        if (cost <= best) {  // (of equal ones the larger tile)
-            best = cost;
-            c.shape = i;
+    constexpr uint32_t k64x128 = 11, k128x64 = 12, k256x128 = 14, k256x256 = 15;
+    auto tiles = [&](uint32_t i) { return fp8_expected_tiles(i, rows, used) * div_up(n, fp8_shape(i).bn); };
+    bool by_rows = false;
+    if (used > 1) {
+        c.shape = rows < 32 * used ? k64x128
+                                   : (rows < 96 * used || tiles(k256x256) < 2 * kGemmCus ? k256x128 : k256x256);
+        by_rows = 4 * tiles(c.shape) >= 3 * kGemmCus;
+    }
+    if (!by_rows) {
+        uint64_t best = ~0ull;
+        for (uint32_t i = 0; i <= kFp8PairIndex; ++i) {
+            if ((silu && fp8_shape(i).bn == 16) || (used > 1 && i == k128x64)) continue;
+            const uint64_t cost = fp8_cost(i, tiles(i));
+            if (cost <= best) {  // (of equal ones the larger tile)
+                best = cost;
+                c.shape = i;
+            }
         }
     }
     const Fp8Shape f = fp8_shape(c.shape);

@@ -46,15 +46,20 @@ __device__ __forceinline__ void wait_stage() {
     __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x0070);
 }
 
+// A value of its own register, which the compiler takes for unknown.
+template <class T>
+__device__ __forceinline__ void keep(T &x) { asm volatile("" : "+v"(x)); }
+
 template <int BM, int BN, int WM, int WN, int RING, int KG>
 struct Fp8Geo {
     static constexpr int kTM = WM / 16, kTN = WN / 16;  // 16 x 16 MFMA tiles per wave
     static constexpr int kWavesN = BN / WN, kWaves = BM / WM * kWavesN;  // of a K group
     static constexpr int kThreads = kWaves * KG * 64, kPerSimd = kWaves * KG > 8 ? 4 : 2;
-    static constexpr int kSegA = BM / 8 / kWaves, kSegW = BN / 8 / kWaves;  // 1 KB copies per wave and stage
+    // 1 KB copies per wave and stage (of fewer A rows than that a copy is made by several waves)
+    static constexpr int kSegA = (BM / 8 + kWaves - 1) / kWaves, kSegW = BN / 8 / kWaves;
     static constexpr int kSegS = (BM / 16 + kWaves - 1) / kWaves;           // 256-byte scale copies per four stages
     static_assert(kTM == 1 || kTM % 2 == 0, "two sets of results in turn");
-    static_assert(BM / 8 % kWaves == 0 && BN / 8 % kWaves == 0, "whole copies");
+    static_assert((BM / 8 % kWaves == 0 || kWaves % (BM / 8) == 0) && BN / 8 % kWaves == 0, "whole copies");
     static constexpr uint32_t kStage = (BM + BN) * kFp8Block;
     static constexpr uint32_t kScales = BM * 4 * 4;
     static constexpr int kCopies = kSegA + kSegW;
@@ -66,16 +71,19 @@ struct Fp8Geo {
     static_assert(KG == 1 || KG * BM * BN * 4 <= kLds, "the groups' sums fit the rings");
 };
 
+// Rows of a product: all of one weight, or an expert's, as they lie or picked by index.
+enum Rows { kDense, kGrouped, kGathered };
+
 // One tile.  rows_a, cols: valid rows and output columns; row0: first output row.
 struct Fp8Tile {
-    const uint8_t *a, *w, *w_up;  // first row of each (a: with GATHER the whole operand)
+    const uint8_t *a, *w, *w_up;  // first row of each (a: with kGathered the whole operand)
     const float *a_s, *w_s, *w_s_up;  // w_s: row of blocks of the first weight row
     const int32_t *index;
     uint32_t rows_a, buf_rows, cols, row0, col0;
     uint32_t tm, tn;  // place of the tile among those that run beside it
 };
 
-template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, bool GATHER>
+template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
 __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t *__restrict__ out, uint32_t out_ld,
                                          uint32_t k, bool wide) {
     using G = Fp8Geo<BM, BN, WM, WN, RING, KG>;
@@ -97,13 +105,13 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     uint32_t oa[G::kSegA], ow[G::kSegW], os[G::kSegS];
     auto source = [&](uint32_t row) -> uint32_t {  // offset, in rows, of tile row `row`; ~0: zeros
         if (row >= t.rows_a) return ~0u;
-        if constexpr (!GATHER) return row;
+        if constexpr (ROWS != kGathered) return row;
         const uint32_t i = (uint32_t)t.index[row];
         return i < t.buf_rows ? i : ~0u;
     };
 #pragma unroll
     for (int i = 0; i < G::kSegA; ++i) {
-        const uint32_t row = (wave + i * G::kWaves) * 8 + lane / 8, src = source(row);
+        const uint32_t row = (wave + i * G::kWaves) % (BM / 8) * 8 + lane / 8, src = source(row);
         oa[i] = src == ~0u ? kPastEnd : src * k + (((lane & 7) ^ chunk_swz(row)) << 4);
     }
 #pragma unroll
@@ -124,7 +132,7 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     auto copy = [&](int i, uint32_t b, uint32_t slot) __attribute__((always_inline)) {
         b = min(first + b, nb - 1);
         if (i < G::kSegA) {
-            char *to = lds + slot * BM * kFp8Block + (wave + i * G::kWaves) * 1024;
+            char *to = lds + slot * BM * kFp8Block + (wave + i * G::kWaves) % (BM / 8) * 1024;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)to, 16, oa[i], b * kFp8Block, 0, 0);
         } else {
             const uint32_t seg = wave + (i - G::kSegA) * G::kWaves;
@@ -192,7 +200,7 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
             wsv = ws[of];
             if constexpr (SILU) wsuv = wsu[of];
         }
-        asm volatile("" : "+v"(wsv), "+v"(wsuv));
+        keep(wsv), keep(wsuv);
     };
     load_w_scales(0);
     copy_scales(0);
@@ -212,7 +220,7 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     const uint32_t base = (uint32_t)(uintptr_t)(lds_void *)lds;
     uint32_t a0 = base + row_a + c0, a1 = base + row_a + c1, w0 = base + row_w + c0, w1 = base + row_w + c1;
     uint32_t sc = base + RING * G::kStage + (wm * WM + c) * 16;
-    asm volatile("" : "+v"(a0), "+v"(a1), "+v"(w0), "+v"(w1), "+v"(sc));
+    keep(a0), keep(a1), keep(w0), keep(w1), keep(sc);
     v8i wf[TN], af[2];
     v4f p[2][TN];
     float s = 0.0f, s2 = 0.0f;  // scales of the 16 rows before
@@ -326,9 +334,14 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     }
 }
 
-// Workgroup -> row tile (of g, none across two experts) and column tile, each XCD a run of
-// neighbours, four row tiles tall (tile_of), that share A and W rows in its L2.
-template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, bool GATHER>
+// (An instance of fp8_tile serves one kernel of a source: the host pass refuses more.)
+// Workgroup -> row tile and column tile.  Dense: each XCD a run of neighbours, four row
+// tiles tall, that share A and W rows in its L2 (tile_of).  Grouped: the experts' tiles
+// are counted from the offsets, so that every XCD gets its share of them, in falling
+// order of work; an expert's last rows, when a half or a quarter of the tile holds them,
+// take waves of as many rows less (8192 rows over 8 uneven experts, n 28672, k 4096:
+// 1157 us in the order of the grid and with whole tiles only).
+template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
 __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
                              (Fp8Geo<BM, BN, WM, WN, RING, KG>::kPerSimd)) void fp8_gemm_kernel(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ w, const float *__restrict__ a_s,
@@ -337,33 +350,57 @@ __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
     __shared__ __attribute__((aligned(1024))) char lds[Fp8Geo<BM, BN, WM, WN, RING, KG>::kLds];
     constexpr uint32_t kCols = SILU ? BN / 2 : BN;
     uint32_t tm, tn;
-    tile_of<4>(blockIdx.x, tiles_m, tiles_n, tm, tn);
-    RowTile r = RowTiles(g, BM, threadIdx.x & 63).find(tm);
-    r.expert = __builtin_amdgcn_readfirstlane(r.expert);
-    r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
-    r.rows = __builtin_amdgcn_readfirstlane(r.rows);
-    if (r.rows == 0) return;
+    RowTile r;
+    if constexpr (ROWS != kDense) {
+        ClassedTiles<BM> rt(g, threadIdx.x & 63);
+        // (overlapping ranges could ask for more tiles than the grid has: those are not computed)
+        tiles_m = min(rt.n0 + rt.n1 + rt.n2, tiles_m);
+        if (blockIdx.x >= tiles_m * tiles_n) return;
+        grouped_tile_of<4>(blockIdx.x, tiles_m, tiles_n, tm, tn);
+        r = rt.find(tm);
+        // the same in every lane; said so, since a buffer descriptor that the compiler
+        // takes for a vector costs a loop around each copy
+        r.expert = __builtin_amdgcn_readfirstlane(r.expert);
+        r.row0 = __builtin_amdgcn_readfirstlane(r.row0);
+        r.rows = __builtin_amdgcn_readfirstlane(r.rows);
+        if (r.rows == 0) return;
+    } else {
+        tile_of<4>(blockIdx.x, tiles_m, tiles_n, tm, tn);
+        r = {0, tm * BM, min((uint32_t)BM, g.rows - tm * BM)};
+    }
     const uint32_t half = n / 2, cols = SILU ? half : n, nb = k / kFp8Block, blocks = (n + kFp8Block - 1) / kFp8Block;
     const uint32_t col0 = __builtin_amdgcn_readfirstlane(tn * kCols);
     const uint64_t wrow = (uint64_t)r.expert * n + col0, wblock = (uint64_t)r.expert * blocks + col0 / kFp8Block;
     Fp8Tile t = {a, w + wrow * k, w + (wrow + half) * k, a_s, w_s + wblock * nb, w_s + (wblock + half / kFp8Block) * nb,
                  nullptr, r.rows, r.rows, min(kCols, cols - col0), r.row0, col0, tm, tn};
-    if constexpr (GATHER) {
+    if constexpr (ROWS == kGathered) {
         t.index = g.index + r.row0;
         t.buf_rows = __builtin_amdgcn_readfirstlane(g.src_rows);
     } else {
         t.a += (uint64_t)r.row0 * k;
         t.a_s += (uint64_t)r.row0 * nb;
     }
-    fp8_tile<BM, BN, WM, WN, RING, KG, SILU, GATHER>(lds, t, out, cols, k, wide);
+    if constexpr (ROWS != kDense && WM >= 64) {
+        if (r.rows <= BM / 4) {
+            fp8_tile<BM / 4, BN, WM / 4, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k, wide);
+            return;
+        }
+    }
+    if constexpr (ROWS != kDense && WM >= 32 && BM >= 64) {
+        if (r.rows <= BM / 2) {
+            fp8_tile<BM / 2, BN, WM / 2, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k, wide);
+            return;
+        }
+    }
+    fp8_tile<BM, BN, WM, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k, wide);
 }
 
-template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, bool GATHER>
+template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
 void launch_kernel(const Fp8Args &p, const Fp8Choice &c, hipStream_t s) {
     using G = Fp8Geo<BM, BN, WM, WN, RING, KG>;
     const uint32_t cols = SILU ? p.n / 2 : p.n;
     const bool wide = cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 8 == 0;
-    hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, WM, WN, RING, KG, SILU, GATHER>), dim3(c.tiles_m * c.tiles_n),
+    hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, WM, WN, RING, KG, SILU, ROWS>), dim3(c.tiles_m * c.tiles_n),
                        dim3(G::kThreads), 0, s, p.a, p.w, p.a_s, p.w_s, p.out, p.rows, p.n, p.k, c.tiles_m, c.tiles_n, wide);
 }
 
@@ -374,15 +411,16 @@ void launch_tile(const Fp8Args &p, const Fp8Choice &c, hipStream_t s) {
     constexpr int BM = F.bm, BN = F.bn;
     static_assert(Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads == F.threads, "what the host counts");
     static_assert(Fp8Geo<BM, BN, WM, WN, RING, KG>::kLds * F.per_cu <= kLdsBytes, "workgroups of a CU");
+    if (p.rows.offsets == nullptr) return launch_kernel<BM, BN, WM, WN, RING, KG, false, kDense>(p, c, s);
     if constexpr (WN > 16) {  // (the SiLU product has gates and ups in one wave)
         if (p.silu) {
-            if (p.rows.index != nullptr) launch_kernel<BM, BN, WM, WN, RING, KG, true, true>(p, c, s);
-            else launch_kernel<BM, BN, WM, WN, RING, KG, true, false>(p, c, s);
+            if (p.rows.index != nullptr) launch_kernel<BM, BN, WM, WN, RING, KG, true, kGathered>(p, c, s);
+            else launch_kernel<BM, BN, WM, WN, RING, KG, true, kGrouped>(p, c, s);
             return;
         }
     }
-    if (p.rows.index != nullptr) launch_kernel<BM, BN, WM, WN, RING, KG, false, true>(p, c, s);
-    else launch_kernel<BM, BN, WM, WN, RING, KG, false, false>(p, c, s);
+    if (p.rows.index != nullptr) launch_kernel<BM, BN, WM, WN, RING, KG, false, kGathered>(p, c, s);
+    else launch_kernel<BM, BN, WM, WN, RING, KG, false, kGrouped>(p, c, s);
 }
 
 }  // namespace fp8_kernels

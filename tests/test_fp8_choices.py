@@ -27,6 +27,8 @@ def choices(tmp_path_factory):
 def test_every_shape_is_tested(choices):
     dense = [c[0] for c in choices([(m, 1, n, k, 0) for m, n, k in gpu.SHAPES])]
     assert sorted(dense) == list(range(NUM_SHAPES)), dense
+    heights = [c[1] for c in choices([(m, 1, 256 * (n // 256 + 1), k, 0) for m, n, k in gpu.SHAPES[8:]])]
+    assert heights == [64, 64, 64, 64, 128, 128, 256, 256, 128], heights  # test_last_rows_of_an_expert
     assert {c[0] for c in choices([(m, 1, n, k, 0) for m, n, k in gpu.DENSE])} >= {-1}
     for silu in (0, 1):
         got = choices([(r, e, 256 * -(-n // 256) if silu else n, k, silu) for r, e, n, k, _ in gpu.GROUPED])

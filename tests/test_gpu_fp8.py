@@ -197,6 +197,26 @@ def test_grouped(rows, experts, n, k, kind, gather, silu):
     check_grouped(got, a, w, a_s, w_s, offsets, index, rows, silu, k)
 
 
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("part", [2, 4, 16])
+@pytest.mark.parametrize("size, height", zip(SHAPES[8:], (64, 64, 64, 64, 128, 128, 256, 256, 128)))
+def test_last_rows_of_an_expert(size, height, part, silu):
+    """Fewer rows used than there is room for: the last tile of one expert holds a half, a quarter, a sixteenth of its
+    rows."""
+    m, n, k = size
+    say("fp8 last rows", m, n, k, part, silu)
+    n = 256 * (n // 256 + 1)
+    rng = np.random.default_rng(m + n + part)
+    used = (m - 1) // height * height + height // part - 1
+    used = used if used <= m else used - height
+    a, w = codes(rng, m, k), codes(rng, 1, n, k)
+    a_s, w_s = scales(rng, m, k // 128) * np.float32(2.0 ** -7), scales(rng, 1, n // 128, k // 128)
+    index = rng.permutation(m)
+    for idx in (None, index):
+        got = run_grouped(a, w, a_s, w_s, np.array([0, used]), idx, m, silu)
+        check_grouped(got, a, w, a_s, w_s, np.array([0, used]), idx, m, silu, k)
+
+
 @pytest.mark.parametrize("offsets", [
     [0, 0, 0, 0, 0], [5, 5, 9, 9, 12], [-3, 4, 4, 100, 7], [40, 3, 3, 2, 1], [0, 300, 300, 300, 300], [2, 290, 1, 1, 1],
     [-(2 ** 31), 2 ** 31 - 1, 0, 0, 0]])
