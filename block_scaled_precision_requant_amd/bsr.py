@@ -478,9 +478,9 @@ def w4a16_group_gemv_experts(x_bf16, w_packed, scale, offsets, out, zero=None, r
 
 
 class MoeScratch:
-    """What the launches of moe_prefill and moe_decode_w4 pass between them, for up to `tokens` tokens of width
-    `hidden`, `experts` experts of which a token takes `top_k`, and expert projections of width `inter`.  Calls that
-    may overlap in time need one each.  It holds the buffers of both calls."""
+    """What the launches of moe_prefill, moe_decode_w4 and moe_prefill_fp8 pass between them, for up to `tokens` tokens
+    of width `hidden`, `experts` experts of which a token takes `top_k`, and expert projections of width `inter`.  Calls
+    that may overlap in time need one each.  It holds the buffers of all three."""
 
     def __init__(self, tokens, experts, top_k, hidden, inter, device="cuda"):
         def buf(*shape, dtype):
@@ -623,11 +623,45 @@ def fp8_grouped_gemm_blockscaled(a_q, w_q, a_scale, w_scale, offsets, out, row_i
 
 def prefill_fp8(a_bf16, w_q, w_scale, a_q_scratch, a_scale_scratch, out, stream=None):
     """The projection on an FP8 weight, in two launches: quantize_act (E4M3, group 128), then fp8_gemm_blockscaled."""
+    m, k = a_bf16.shape
     dev = a_bf16.get_device()
-    _arg(a_bf16, (out.shape[0], w_q.shape[1]), BF16, "a_bf16", dev)
+    _arg(a_bf16, (m, k), BF16, "a_bf16", dev)  # (all of the second launch's arguments are looked at before the first)
+    _e4m3(a_q_scratch, (m, k), "a_q_scratch", dev)
+    _arg(a_scale_scratch, (m, k // 128), F32, "a_scale_scratch", dev)
+    n = w_q.shape[0]
+    _e4m3(w_q, (n, k), "w_q", dev)
+    _arg(w_scale, (-(-n // 128), k // 128), F32, "w_scale", dev)
+    _arg(out, (m, n), BF16, "out", dev)
     with _on(dev):
         quantize_act(a_bf16, a_q_scratch, a_scale_scratch, group=128, fmt=FMT_E4M3, stream=stream)
     fp8_gemm_blockscaled(a_q_scratch, w_q, a_scale_scratch, w_scale, out, stream=stream)
+
+
+def moe_prefill_fp8(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale, out, scratch, residual=None,
+                    score=SCORE_SOFTMAX, renorm=True, scale=1.0, stream=None):
+    """One expert layer on FP8 weights (quantize_w_fp8), for any number of tokens: as moe_prefill, with w_gate_up
+    [E,2I,H] and w_down [E,H,I] in E4M3 codes and their scales (H and I multiples of 128), in six steps: router,
+    activation quantizer, grouped gate and up with the SiLU product, its quantizer, grouped down, weighted sum."""
+    t, (hidden, inter) = _layer_tokens(x_bf16, logits, out, residual), w_down.shape[1:]
+    if hidden % 128 or inter % 128:
+        raise ValueError(f"w_down: shape {tuple(w_down.shape)}, its last two sizes must be multiples of 128")
+    s = scratch
+    rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
+
+    def codes(q, q_scale, n, width):  # of n rows, in the scratch of the int8 layer: bytes, and fewer scales
+        return q[:n].view(torch.uint8), q_scale.view(-1)[:n * (width // 128)].view(n, width // 128)
+
+    a_q, a_scale = codes(s.a_i8, s.a_scale, t, hidden)
+    h_q, h_scale = codes(s.h_i8, s.h_scale, rows, inter)
+    h, y, dev = s.h[:rows], s.y[:rows], x_bf16.get_device()
+    with _on(dev):  # (the quantizers run on the current device)
+        quantize_act(x_bf16, a_q, a_scale, group=128, fmt=FMT_E4M3, stream=stream)
+    fp8_grouped_gemm_blockscaled(a_q, w_gate_up, a_scale, gate_up_scale, s.offsets, h, row_index=s.row_token[:rows],
+                                 silu_mul=True, stream=stream)
+    with _on(dev):
+        quantize_act(h, h_q, h_scale, group=128, fmt=FMT_E4M3, stream=stream)
+    fp8_grouped_gemm_blockscaled(h_q, w_down, h_scale, down_scale, s.offsets, y, stream=stream)
+    moe_combine(y, s.pos[:t], s.weights[:t], out, residual=residual, stream=stream)
 
 
 def moe_dispatch(x, pos, out, stream=None):
