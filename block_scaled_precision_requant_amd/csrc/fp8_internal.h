@@ -51,6 +51,28 @@ __device__ __forceinline__ v4f fp8_dot16(v8i w, v8i a) {
 // gate / (1 + exp(-gate)) * up; for gate below -88 the quotient is -0.
 __device__ __forceinline__ float silu_product(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
 
+// Eight elements of a row of n, from c on; rows of any alignment (one 16-byte access at
+// any even address where all eight are there, else element by element).
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8), aligned(2)));
+
+__device__ __forceinline__ u16x8 load8(const uint16_t *p, uint32_t c, uint32_t n) {
+    if (c + 8 <= n) return *reinterpret_cast<const u16x8 *>(p + c);
+    u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (c + i < n) v[i] = p[c + i];
+    return v;
+}
+__device__ __forceinline__ void store8(uint16_t *p, uint32_t c, uint32_t n, u16x8 v) {
+    if (c + 8 <= n) {
+        *reinterpret_cast<u16x8 *>(p + c) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (c + i < n) p[c + i] = v[i];
+}
+
 // Four columns of one output row, those below n.  `wide`: out and n keep 8-byte words whole.
 __device__ __forceinline__ void store4(uint16_t *out, uint64_t row, uint32_t col, uint32_t n, v4f v, bool wide) {
     uint16_t *p = out + row * n + col;

@@ -202,12 +202,12 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
         }
         keep(wsv), keep(wsuv);
     };
-    load_w_scales(0);
     copy_scales(0);
 #pragma unroll
     for (int r = 0; r < RING - 1; ++r)
 #pragma unroll
         for (int x = 0; x < kCopies; ++x) copy(x, r, r);
+    load_w_scales(0);
     // (a group of one wave reads only what it copied itself)
     auto meet = [&]() __attribute__((always_inline)) {
         if constexpr (G::kWaves > 1) stage_barrier();
@@ -221,7 +221,10 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     uint32_t a0 = base + row_a + c0, a1 = base + row_a + c1, w0 = base + row_w + c0, w1 = base + row_w + c1;
     uint32_t sc = base + RING * G::kStage + (wm * WM + c) * 16;
     keep(a0), keep(a1), keep(w0), keep(w1), keep(sc);
-    v8i wf[TN], af[2];
+    constexpr bool kAll = TM <= 4 && TM > 1;
+    constexpr int kAf = kAll ? TM : 2;
+    v8i wf[TN], af[kAf];
+    float sas[TM];
     v4f p[2][TN];
     float s = 0.0f, s2 = 0.0f;  // scales of the 16 rows before
 #pragma unroll
@@ -240,12 +243,18 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const float sa = *reinterpret_cast<const lds_float *>(sc + i * 256);
+            if (kAll && i == 0) {
+#pragma unroll
+                for (int x = 0; x < TM; ++x) sas[x] = *reinterpret_cast<const lds_float *>(sc + x * 256);
+#pragma unroll
+                for (int x = 1; x < TM; ++x) af[x % kAf] = operand(a0, a1, x);
+            }
+            const float sa = kAll ? sas[i] : *reinterpret_cast<const lds_float *>(sc + i * 256);
             if constexpr (TM == 1)
 #pragma unroll
                 for (int x = 0; x < kCopies; ++x) copy(x, b + RING - 1, free_slot);
             if (i + 1 < TM) {
-                af[(i + 1) & 1] = operand(a0, a1, i + 1);
+                if (!kAll) af[(i + 1) & 1] = operand(a0, a1, i + 1);
             } else {
                 wait_stage<(RING - 2) * kCopies + (G::kTouch ? 2 : 0)>();
                 meet();
@@ -270,7 +279,7 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
 #pragma unroll
                 for (int x = 0; x < kCopies; ++x)
                     if (x * kSlots / kCopies == i * TN + j) copy(x, b + RING - 1, free_slot);
-                p[i & 1][j] = fp8_dot16(wf[j], af[i & 1]);
+                p[i & 1][j] = fp8_dot16(wf[j], af[i % kAf]);
                 if (i + 1 == TM) wf[j] = operand(w0, w1, j);
                 if (i + 1 == TM && j + 1 == TN) af[0] = operand(a0, a1, 0);
 #pragma unroll
@@ -318,6 +327,37 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
                 acc[i][j] = v;
             }
         }
+    }
+    if constexpr (KG == 1) {
+        // Each wave turns its outputs through LDS of its own, so that a store writes whole
+        // rows of the wave's columns, 16 bytes a lane (in the layout of the products a
+        // store of 8 bytes a lane touches 16 rows, at a quarter of the rate: 8192 x 28672
+        // outputs, k 4096, 876 us against 790).  16-byte chunk x of row r sits at x ^ (r % kChunks).
+        constexpr uint32_t kRow = kWaveCols * 2, kChunks = kRow / 16;
+        static_assert(G::kWaves * WM * kRow <= G::kLds, "the outputs fit the ring");
+        __syncthreads();  // every wave's copies have landed
+        char *mine = smem + wave * WM * kRow;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < (SILU ? TN / 2 : TN); ++j) {
+                v4f v = acc[i][j];
+                if constexpr (SILU)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = silu_product(v[r], acc[i][j + TN / 2][r]);
+                const uint32_t row = i * 16 + c, chunk = (2 * j + q / 2) ^ (row % kChunks);
+                *reinterpret_cast<ushort4 *>(mine + row * kRow + chunk * 16 + q % 2 * 8) =
+                    make_ushort4(f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3]));
+            }
+#pragma unroll
+        for (uint32_t r0 = 0; r0 < WM; r0 += 64 / kChunks) {
+            const uint32_t row = r0 + lane / kChunks, chunk = lane % kChunks;
+            const v4i v = *reinterpret_cast<const v4i *>(mine + row * kRow + (chunk ^ (row % kChunks)) * 16);
+            if (wm * WM + row < t.rows_a)
+                store8(out + (uint64_t)(t.row0 + wm * WM + row) * out_ld, first_col + chunk * 8, out_ld,
+                       __builtin_bit_cast(u16x8, v));
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {

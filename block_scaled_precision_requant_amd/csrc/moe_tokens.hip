@@ -15,28 +15,6 @@
 namespace bsr {
 namespace {
 
-// Eight columns from column c on; rows of any alignment (`whole`: all eight are
-// below n, one 16-byte access at any address; else element by element).
-typedef uint16_t u16x8 __attribute__((ext_vector_type(8), aligned(2)));
-
-__device__ __forceinline__ u16x8 load8(const uint16_t *p, uint32_t c, uint32_t n) {
-    if (c + 8 <= n) return *reinterpret_cast<const u16x8 *>(p + c);
-    u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (c + i < n) v[i] = p[c + i];
-    return v;
-}
-__device__ __forceinline__ void store8(uint16_t *p, uint32_t c, uint32_t n, u16x8 v) {
-    if (c + 8 <= n) {
-        *reinterpret_cast<u16x8 *>(p + c) = v;
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (c + i < n) p[c + i] = v[i];
-}
-
 __global__ __launch_bounds__(kTokenThreads) void dispatch_kernel(const uint16_t *__restrict__ x,
                                                                  const int32_t *__restrict__ pos,
                                                                  uint16_t *__restrict__ out, uint32_t top_k,
