@@ -80,7 +80,7 @@ struct Fp8Tile {
     const float *a_s, *w_s, *w_s_up;  // w_s: row of blocks of the first weight row
     const int32_t *index;
     uint32_t rows_a, buf_rows, cols, row0, col0;
-    uint32_t tm, tn;  // place of the tile among those that run beside it
+    uint32_t tall, place, tn;  // rows of tiles that run together, which of them this is, and its column of tiles
 };
 
 template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
@@ -159,12 +159,15 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     // for the cache behind the L2, whose latency is a stage long.
     uint32_t ta = kPastEnd, tw = kPastEnd;
     if constexpr (G::kTouch) {
-        constexpr uint32_t kShareA = BM / 8 / G::kWaves, kShareW = BN / 4 / G::kWaves;
-        const uint32_t src = source((t.tn % 8 * G::kWaves + wave) * kShareA + lane);
-        if (lane < kShareA && src != ~0u) ta = src * k;
+        const uint32_t beside = max(32 / t.tall, 1u);  // tiles beside one another that share the A rows
+        const uint32_t per_a = (BM / G::kWaves + beside - 1) / beside, src_row = (t.tn % beside * G::kWaves + wave) * per_a + lane;
+        const uint32_t src = src_row < BM ? source(src_row) : ~0u;
+        if (lane < per_a && src != ~0u) ta = src * k;
         // (with the SiLU product even waves take gate rows and odd ones up rows)
-        if (lane < kShareW)
-            tw = ((SILU ? t.tm % 4 * (G::kWaves / 2) + wave / 2 : t.tm % 4 * G::kWaves + wave) * kShareW + lane) * k;
+        constexpr uint32_t kWavesW = SILU ? G::kWaves / 2 : G::kWaves, kRowsW = SILU ? BN / 2 : BN;
+        const uint32_t per_w = (kRowsW / kWavesW + t.tall - 1) / t.tall;
+        const uint32_t row_w = (t.place * kWavesW + (SILU ? wave / 2 : wave)) * per_w + lane;
+        if (lane < per_w && row_w < kRowsW) tw = row_w * k;
     }
     auto touch = [&](uint32_t b) __attribute__((always_inline)) {
         b = min(b, nb - 1);
@@ -374,6 +377,49 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
     }
 }
 
+// The v-th tile: an expert's whole tiles down its rows, then along its columns, in
+// groups of up to six rows of tiles, so that what runs together shares A and W rows; then
+// the experts' last rows along their columns.
+template <uint32_t BM>
+__device__ __forceinline__ RowTile place_tile(ClassedTiles<BM> &rt, uint32_t v, uint32_t tiles_n, uint32_t &tall,
+                                              uint32_t &place, uint32_t &tn) {
+    tall = 1;
+    place = 0;
+    uint32_t u = v / tiles_n;
+    tn = v % tiles_n;
+    if (u >= rt.n0) return rt.find(u);
+    uint32_t local = v;  // within the expert's tiles
+    for (uint32_t e0 = 0;;) {
+        const uint64_t past = __ballot(rt.full_incl > u);
+        if (past != 0) {
+            const int o = __builtin_ctzll(past);
+            const uint32_t rows = __builtin_amdgcn_readlane(rt.full, o);
+            const uint32_t olo = __builtin_amdgcn_readlane(rt.lo, o), ohi = __builtin_amdgcn_readlane(rt.hi, o);
+            local -= (__builtin_amdgcn_readlane(rt.full_incl, o) - rows) * tiles_n;
+            const uint32_t groups = (rows + 5) / 6, size = (rows + groups - 1) / groups;
+            const uint32_t first = local / (size * tiles_n) * size, in = local % (size * tiles_n);
+            tall = min(size, rows - first);
+            place = in % tall;
+            tn = in / tall;
+            const uint32_t row0 = olo + (first + place) * BM;
+            return {e0 + o, row0, min(BM, ohi - row0)};
+        }
+        const uint32_t all = __builtin_amdgcn_readlane(rt.full_incl, 63);
+        u -= all;
+        local -= all * tiles_n;
+        e0 += 64;
+        if (e0 >= rt.g.experts) return {0, 0, 0};
+        rt.load(e0);
+    }
+}
+
+// Workgroup -> which tile: each XCD takes runs of 32 in turn.
+__device__ __forceinline__ uint32_t grouped_run(uint32_t wg, uint32_t total) {
+    uint32_t tm, tn;
+    grouped_tile_of<1>(wg, total, 1, tm, tn);
+    return tm;
+}
+
 // (An instance of fp8_tile serves one kernel of a source: the host pass refuses more.)
 // Workgroup -> row tile and column tile.  Dense: each XCD a run of neighbours, four row
 // tiles tall, that share A and W rows in its L2 (tile_of).  Grouped: the experts' tiles
@@ -389,15 +435,17 @@ __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
     uint32_t tiles_m, uint32_t tiles_n, bool wide) {
     __shared__ __attribute__((aligned(1024))) char lds[Fp8Geo<BM, BN, WM, WN, RING, KG>::kLds];
     constexpr uint32_t kCols = SILU ? BN / 2 : BN;
-    uint32_t tm, tn;
+    uint32_t tn, tall = 4, place;
     RowTile r;
     if constexpr (ROWS != kDense) {
         ClassedTiles<BM> rt(g, threadIdx.x & 63);
         // (overlapping ranges could ask for more tiles than the grid has: those are not computed)
         tiles_m = min(rt.n0 + rt.n1 + rt.n2, tiles_m);
         if (blockIdx.x >= tiles_m * tiles_n) return;
-        grouped_tile_of<4>(blockIdx.x, tiles_m, tiles_n, tm, tn);
-        r = rt.find(tm);
+        r = place_tile(rt, grouped_run(blockIdx.x, tiles_m * tiles_n), tiles_n, tall, place, tn);
+        tall = __builtin_amdgcn_readfirstlane(tall);
+        place = __builtin_amdgcn_readfirstlane(place);
+        tn = __builtin_amdgcn_readfirstlane(tn);
         // the same in every lane; said so, since a buffer descriptor that the compiler
         // takes for a vector costs a loop around each copy
         r.expert = __builtin_amdgcn_readfirstlane(r.expert);
@@ -405,14 +453,16 @@ __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
         r.rows = __builtin_amdgcn_readfirstlane(r.rows);
         if (r.rows == 0) return;
     } else {
+        uint32_t tm;
         tile_of<4>(blockIdx.x, tiles_m, tiles_n, tm, tn);
+        place = tm % 4;
         r = {0, tm * BM, min((uint32_t)BM, g.rows - tm * BM)};
     }
     const uint32_t half = n / 2, cols = SILU ? half : n, nb = k / kFp8Block, blocks = (n + kFp8Block - 1) / kFp8Block;
     const uint32_t col0 = __builtin_amdgcn_readfirstlane(tn * kCols);
     const uint64_t wrow = (uint64_t)r.expert * n + col0, wblock = (uint64_t)r.expert * blocks + col0 / kFp8Block;
     Fp8Tile t = {a, w + wrow * k, w + (wrow + half) * k, a_s, w_s + wblock * nb, w_s + (wblock + half / kFp8Block) * nb,
-                 nullptr, r.rows, r.rows, min(kCols, cols - col0), r.row0, col0, tm, tn};
+                 nullptr, r.rows, r.rows, min(kCols, cols - col0), r.row0, col0, tall, place, tn};
     if constexpr (ROWS == kGathered) {
         t.index = g.index + r.row0;
         t.buf_rows = __builtin_amdgcn_readfirstlane(g.src_rows);
