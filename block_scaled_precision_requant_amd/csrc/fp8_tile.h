@@ -68,7 +68,6 @@ struct Fp8Geo {
     static constexpr uint32_t kGroupLds = RING * kStage + 2 * kScales + (kTouch ? 256 : 0), kLds = KG * kGroupLds;
     // (what is waited for counts copies of whole stages; a scale copy is behind those of three)
     static_assert(RING >= 2 && RING <= 6 && (RING - 2) * kCopies + 2 < 64, "copies in flight");
-    static_assert(KG == 1 || KG * BM * BN * 4 <= kLds, "the groups' sums fit the rings");
 };
 
 // Rows of a product: all of one weight, or an expert's, as they lie or picked by index.
@@ -85,7 +84,7 @@ struct Fp8Tile {
 
 template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
 __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t *__restrict__ out, uint32_t out_ld,
-                                         uint32_t k, bool wide) {
+                                         uint32_t k) {
     using G = Fp8Geo<BM, BN, WM, WN, RING, KG>;
     constexpr int TM = G::kTM, TN = G::kTN;
     constexpr uint32_t kWaveCols = SILU ? WN / 2 : WN;
@@ -310,10 +309,11 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
         for (int r = 0; r < 4; ++r)
             if (TM > 1) acc[TM - 1][j][r] = fmaf(p[1][j][r], SILU && j >= TN / 2 ? s2 : s, acc[TM - 1][j][r]);
 
+    constexpr uint32_t kSums = KG > 1 ? KG * BM * BN * 4 : 0;
+    __syncthreads();  // every wave's copies have landed: the rings are free
     if constexpr (KG > 1) {
         // the groups' sums, added in group order, each group a share of the tiles
         v4f *sums = reinterpret_cast<v4f *>(smem);
-        __syncthreads();  // (the rings are free)
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -331,48 +331,35 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
             }
         }
     }
-    if constexpr (KG == 1) {
-        // Each wave turns its outputs through LDS of its own, so that a store writes whole
-        // rows of the wave's columns, 16 bytes a lane (in the layout of the products a
-        // store of 8 bytes a lane touches 16 rows, at a quarter of the rate: 8192 x 28672
-        // outputs, k 4096, 876 us against 790).  16-byte chunk x of row r sits at x ^ (r % kChunks).
-        constexpr uint32_t kRow = kWaveCols * 2, kChunks = kRow / 16;
-        static_assert(G::kWaves * WM * kRow <= G::kLds, "the outputs fit the ring");
-        __syncthreads();  // every wave's copies have landed
-        char *mine = smem + wave * WM * kRow;
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < (SILU ? TN / 2 : TN); ++j) {
-                v4f v = acc[i][j];
-                if constexpr (SILU)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = silu_product(v[r], acc[i][j + TN / 2][r]);
-                const uint32_t row = i * 16 + c, chunk = (2 * j + q / 2) ^ (row % kChunks);
-                *reinterpret_cast<ushort4 *>(mine + row * kRow + chunk * 16 + q % 2 * 8) =
-                    make_ushort4(f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3]));
-            }
-#pragma unroll
-        for (uint32_t r0 = 0; r0 < WM; r0 += 64 / kChunks) {
-            const uint32_t row = r0 + lane / kChunks, chunk = lane % kChunks;
-            const v4i v = *reinterpret_cast<const v4i *>(mine + row * kRow + (chunk ^ (row % kChunks)) * 16);
-            if (wm * WM + row < t.rows_a)
-                store8(out + (uint64_t)(t.row0 + wm * WM + row) * out_ld, first_col + chunk * 8, out_ld,
-                       __builtin_bit_cast(u16x8, v));
-        }
-        return;
-    }
+    // Each wave turns its outputs through LDS of its own, so that a store writes whole
+    // rows of the wave's columns, 16 bytes a lane (in the layout of the products a store
+    // of 8 bytes a lane touches 16 rows, at a quarter of the rate: 8192 x 28672 outputs, k
+    // 4096, 876 us against 828; 2048 x 4095, 48 against 38).  16-byte chunk x of row r sits
+    // at x ^ (r % kChunks).
+    constexpr uint32_t kRow = kWaveCols * 2, kChunks = kRow / 16, kOwn = (TM + KG - 1) / KG * 16;
+    static_assert(kSums + KG * G::kWaves * kOwn * kRow <= G::kLds, "the outputs fit beside the sums");
+    char *mine = smem + kSums + (group * G::kWaves + wave) * kOwn * kRow;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const uint32_t row = wm * WM + i * 16 + c;
-        if (row >= t.rows_a || (KG > 1 && i % KG != group)) continue;
+        if (KG > 1 && i % KG != group) continue;
 #pragma unroll
         for (int j = 0; j < (SILU ? TN / 2 : TN); ++j) {
             v4f v = acc[i][j];
             if constexpr (SILU)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = silu_product(v[r], acc[i][j + TN / 2][r]);
-            store4(out, t.row0 + row, first_col + j * 16 + 4 * q, out_ld, v, wide);
+            const uint32_t row = i / KG * 16 + c, chunk = (2 * j + q / 2) ^ (row % kChunks);
+            *reinterpret_cast<ushort4 *>(mine + row * kRow + chunk * 16 + q % 2 * 8) =
+                make_ushort4(f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3]));
+        }
+    }
+#pragma unroll
+    for (uint32_t r0 = 0; r0 < kOwn; r0 += 64 / kChunks) {
+        const uint32_t own = r0 + lane / kChunks, chunk = lane % kChunks;
+        const uint32_t tile = own / 16 * KG + group, row = wm * WM + tile * 16 + own % 16;
+        if (own < kOwn && tile < TM && row < t.rows_a) {
+            const v4i v = *reinterpret_cast<const v4i *>(mine + own * kRow + (chunk ^ (own % kChunks)) * 16);
+            store8(out + (uint64_t)(t.row0 + row) * out_ld, first_col + chunk * 8, out_ld, __builtin_bit_cast(u16x8, v));
         }
     }
 }
@@ -432,7 +419,7 @@ __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
                              (Fp8Geo<BM, BN, WM, WN, RING, KG>::kPerSimd)) void fp8_gemm_kernel(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ w, const float *__restrict__ a_s,
     const float *__restrict__ w_s, uint16_t *__restrict__ out, GroupedRows g, uint32_t n, uint32_t k,
-    uint32_t tiles_m, uint32_t tiles_n, bool wide) {
+    uint32_t tiles_m, uint32_t tiles_n) {
     __shared__ __attribute__((aligned(1024))) char lds[Fp8Geo<BM, BN, WM, WN, RING, KG>::kLds];
     constexpr uint32_t kCols = SILU ? BN / 2 : BN;
     uint32_t tn, tall = 4, place;
@@ -472,26 +459,24 @@ __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
     }
     if constexpr (ROWS != kDense && WM >= 64) {
         if (r.rows <= BM / 4) {
-            fp8_tile<BM / 4, BN, WM / 4, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k, wide);
+            fp8_tile<BM / 4, BN, WM / 4, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k);
             return;
         }
     }
     if constexpr (ROWS != kDense && WM >= 32 && BM >= 64) {
         if (r.rows <= BM / 2) {
-            fp8_tile<BM / 2, BN, WM / 2, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k, wide);
+            fp8_tile<BM / 2, BN, WM / 2, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k);
             return;
         }
     }
-    fp8_tile<BM, BN, WM, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k, wide);
+    fp8_tile<BM, BN, WM, WN, RING, KG, SILU, ROWS>(lds, t, out, cols, k);
 }
 
 template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
 void launch_kernel(const Fp8Args &p, const Fp8Choice &c, hipStream_t s) {
     using G = Fp8Geo<BM, BN, WM, WN, RING, KG>;
-    const uint32_t cols = SILU ? p.n / 2 : p.n;
-    const bool wide = cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 8 == 0;
     hipLaunchKernelGGL((fp8_gemm_kernel<BM, BN, WM, WN, RING, KG, SILU, ROWS>), dim3(c.tiles_m * c.tiles_n),
-                       dim3(G::kThreads), 0, s, p.a, p.w, p.a_s, p.w_s, p.out, p.rows, p.n, p.k, c.tiles_m, c.tiles_n, wide);
+                       dim3(G::kThreads), 0, s, p.a, p.w, p.a_s, p.w_s, p.out, p.rows, p.n, p.k, c.tiles_m, c.tiles_n);
 }
 
 // The shape of index S, by waves of WM x WN.
