@@ -37,18 +37,17 @@ constexpr uint32_t kFp8PairIndex = kFp8NumShapes;
 BSR_HD constexpr Fp8Shape fp8_shape(uint32_t i) { return i == kFp8PairIndex ? kFp8Pair : kFp8Shapes[i]; }
 
 // ---- product, the weight streamed into registers ------------------------------
-// A workgroup owns 16 rows by 16 ct columns; its waves split K in chunks of 128, two of
+// A workgroup owns 16 rows by 16 columns (and as many of the up half); its waves split K in chunks of 128, two of
 // them in flight.
 constexpr uint32_t kFp8MaxWaves = 8;
 constexpr uint32_t kFp8Few = 4;  // rows (of an expert, on average) up to which it runs
 
 struct Fp8StreamPlan {
-    uint32_t ct, row_tiles, col_tiles, waves, chunks_per_wave, lds;
+    uint32_t row_tiles, col_tiles, waves, chunks_per_wave, lds;
 };
 
 inline Fp8StreamPlan fp8_stream_plan(uint32_t rows, uint32_t experts, uint32_t cols, uint32_t k, bool silu) {
     Fp8StreamPlan p;
-    p.ct = silu ? 2 : 1;
     p.row_tiles = (uint32_t)grouped_row_tiles(rows, experts, 16);
     p.col_tiles = (uint32_t)div_up(cols, 16);
     const uint32_t chunks = k / kFp8Block;
@@ -58,7 +57,7 @@ inline Fp8StreamPlan fp8_stream_plan(uint32_t rows, uint32_t experts, uint32_t c
     waves = waves < chunks ? waves : chunks;
     p.chunks_per_wave = (uint32_t)div_up(chunks, waves);
     p.waves = (uint32_t)div_up(chunks, p.chunks_per_wave);
-    p.lds = p.waves * p.ct * 64 * 16;
+    p.lds = p.waves * (silu ? 2 : 1) * 64 * 16;
     return p;
 }
 

@@ -1,25 +1,35 @@
-// fp8_stream.hip -- the FP8 products for few rows (dense, or per expert), where
+// fp8_stream.hip -- the FP8 products for one to a few rows (dense, or per expert), where
 // reading the weight once is all the time there is.
 //
 // out[i,j] = sum_b fl32(a_s[i,b] * w_s[j/128,b]) * P[i,j,b], P the dot product of
-// block b.  A workgroup owns 16 MT rows by 16 CT columns and its waves split K.  A
-// scale block is one K step of v_mfma_f32_16x16x128_f8f6f4, whose operand is 32
-// consecutive codes of a row per lane: the weight rows, and the activations beside
-// them, stream from memory straight into the registers that the matrix core reads
-// -- no LDS, no swap, no barrier before the end -- two chunks of 128 in flight while
-// the two before them are computed.  The weight is the matrix core's row operand, so
-// a lane holds four columns of one activation row, whose scale is one value per lane,
-// and the weight's is one per wave: a block ends with one product and four FMAs per
-// 16 x 16 outputs.  At the end the waves' sums are added in wave order through LDS.
+// block b.  A workgroup owns 16 rows by 16 columns (with the SiLU product 16 of the gate
+// and 16 of the up half) and its waves split K.  A scale block is one K step of
+// v_mfma_f32_16x16x128_f8f6f4 (what it adds in fewer than 32 bits: fp8_tile.h), whose
+// operand is 32 consecutive codes of a row per lane: the weight rows, and the activations
+// beside them, stream from memory straight into the registers that the matrix core reads
+// -- no LDS, no swap, no barrier before the end -- two chunks of 128 in flight while the
+// two before them are computed.  The weight is the matrix core's row operand, so a lane
+// holds four columns of one activation row, whose scale is one value per lane, and the
+// weight's is one per wave.  At the end the waves' sums are added in wave order through
+// LDS.
+//
+// In this layout a load touches 16 rows and moves 16 bytes a clock and CU, 9.7 TB/s over
+// the chip: enough for the weight alone, which is why rows past kFp8Few run in the tiles
+// of fp8_tile.h.  MI355X: one row, n 28672, k 4096 / 8192 (117 / 235 MB) 23.6 / 46.7 us,
+// 5.0 TB/s, as a device copy of 1 GiB reaches; n 4096, k 14336 (59 MB, which the 256 MB
+// cache holds between calls) 11.2 us; 256 rows through the gate and up projections of 64
+// uneven experts, n 4096, k 2048, 83 us.
 #include "fp8_internal.h"
 
 namespace bsr {
 namespace {
 
-template <int MT, int CT, int PASS>
+constexpr int kPass = 2;  // chunks in flight
+
+template <int CT>
 struct Fp8Pass {
-    v8i w[PASS][CT], a[PASS][MT];
-    float s[PASS][MT];
+    v8i w[kPass][CT], a[kPass];
+    float s[kPass];
 };
 
 __device__ __forceinline__ v8i load32(__amdgpu_buffer_rsrc_t r, uint32_t lane_offset, uint32_t offset) {
@@ -27,29 +37,24 @@ __device__ __forceinline__ v8i load32(__amdgpu_buffer_rsrc_t r, uint32_t lane_of
                                    5, 6, 7);
 }
 
-template <int MT, int CT, int PASS, bool SILU>
+template <bool SILU>
 __global__ __launch_bounds__(kFp8MaxWaves * 64, 2) void fp8_stream_kernel(
     const uint8_t *__restrict__ a, const uint8_t *__restrict__ w, const float *__restrict__ a_s,
     const float *__restrict__ w_s, uint16_t *__restrict__ out, GroupedRows g, uint32_t n, uint32_t k,
-    uint32_t row_tiles, uint32_t col_tiles, uint32_t chunks_per_wave, bool wide) {
+    uint32_t col_tiles, uint32_t chunks_per_wave, bool wide) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    static_assert(!SILU || CT % 2 == 0, "gate and up tiles");
-    constexpr uint32_t kCols = 16 * (SILU ? CT / 2 : CT);  // output columns of the workgroup
+    constexpr int CT = SILU ? 2 : 1;  // weight tiles: a gate and an up tile
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nwaves = blockDim.x >> 6;
-    const uint32_t wg = blockIdx.x;
-    // (dense: row tiles side by side, which share their weight columns)
-    const uint32_t tm = g.offsets == nullptr ? wg % row_tiles : wg / col_tiles;
-    const uint32_t tn = g.offsets == nullptr ? wg / row_tiles : wg % col_tiles;
-    RowTile t = RowTiles(g, 16 * MT, lane).find(tm);
+    RowTile t = RowTiles(g, 16, lane).find(blockIdx.x / col_tiles);
     t.expert = __builtin_amdgcn_readfirstlane(t.expert);
     t.row0 = __builtin_amdgcn_readfirstlane(t.row0);
     t.rows = __builtin_amdgcn_readfirstlane(t.rows);
     if (t.rows == 0) return;
     const uint32_t c = lane & 15, q = lane >> 4, nb = k / kFp8Block;
-    const uint32_t col0 = tn * kCols, half = n / 2, cols = SILU ? half : n;
-    const uint32_t live = min(cols - col0, kCols);
+    const uint32_t col0 = blockIdx.x % col_tiles * 16, half = n / 2, cols = SILU ? half : n;
+    const uint32_t live = min(cols - col0, 16u);
     const uint32_t first = wave * chunks_per_wave, end = min(nb, first + chunks_per_wave);
 
     // descriptors and scalar offsets, the same in all lanes, and a 32-bit offset per
@@ -66,54 +71,36 @@ __global__ __launch_bounds__(kFp8MaxWaves * 64, 2) void fp8_stream_kernel(
     const uint64_t a0 = g.index != nullptr ? 0 : t.row0;
     const auto ra = __builtin_amdgcn_make_buffer_rsrc((void *)(a + a0 * k), (short)0, (int)(arows * k), kRsrcWord3);
     const auto rs = __builtin_amdgcn_make_buffer_rsrc((void *)(a_s + a0 * nb), (short)0, (int)(arows * nb * 4), kRsrcWord3);
-    uint32_t ao[MT], so[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const uint32_t r = 16 * i + c;
-        uint32_t src = ~0u;
-        if (r < t.rows) src = g.index != nullptr ? (uint32_t)g.index[t.row0 + r] : r;
-        ao[i] = src < arows ? src * k + 32 * q : kPastEnd;
-        so[i] = src < arows ? src * nb * 4 : kPastEnd;
-    }
+    uint32_t src = ~0u;
+    if (c < t.rows) src = g.index != nullptr ? (uint32_t)g.index[t.row0 + c] : c;
+    const uint32_t ao = src < arows ? src * k + 32 * q : kPastEnd;
+    const uint32_t so = src < arows ? src * nb * 4 : kPastEnd;
 
-    using Pass = Fp8Pass<MT, CT, PASS>;
+    using Pass = Fp8Pass<CT>;
     // chunks from `chunk` on; past the wave's last one that is read again, and counts 0
     auto load = [&](Pass &b, uint32_t chunk) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < PASS; ++i) {
+        for (int i = 0; i < kPass; ++i) {
             const uint32_t at = min(chunk + i, end - 1);
 #pragma unroll
-            for (int j = 0; j < CT; ++j)
-                b.w[i][j] = SILU && j >= CT / 2 ? load32(ru, wo + 16 * (j - CT / 2) * k, at * kFp8Block)
-                                                : load32(rw, wo + 16 * j * k, at * kFp8Block);
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                b.a[i][j] = load32(ra, ao[j], at * kFp8Block);
-                b.s[i][j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, so[j], at * 4, 0));
-            }
+            for (int j = 0; j < CT; ++j) b.w[i][j] = load32(j == 0 ? rw : ru, wo, at * kFp8Block);
+            b.a[i] = load32(ra, ao, at * kFp8Block);
+            b.s[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, so, at * 4, 0));
         }
     };
-    v4f acc[MT][CT];
+    v4f acc[CT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < CT; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+    for (int j = 0; j < CT; ++j) acc[j] = v4f{0, 0, 0, 0};
     auto compute = [&](const Pass &b, uint32_t chunk) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < PASS; ++i) {
+        for (int i = 0; i < kPass; ++i) {
             const uint32_t at = min(chunk + i, end - 1);
-            const float sw = ws[at], su = SILU ? wsu[at] : sw;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const float sa = chunk + i < end ? b.s[i][j] : 0.0f;
-                const float s = chunk + i < end ? sa * sw : 0.0f, s2 = chunk + i < end ? sa * su : 0.0f;
+            for (int j = 0; j < CT; ++j) {
+                const float s = chunk + i < end ? b.s[i] * (j == 0 ? ws[at] : wsu[at]) : 0.0f;
+                const v4f p = fp8_dot16(b.w[i][j], b.a[i]);
 #pragma unroll
-                for (int l = 0; l < CT; ++l) {
-                    const v4f p = fp8_dot16(b.w[i][l], b.a[i][j]);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[j][l][r] = fmaf(p[r], SILU && l >= CT / 2 ? s2 : s, acc[j][l][r]);
-                }
+                for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(p[r], s, acc[j][r]);
             }
         }
     };
@@ -121,12 +108,12 @@ __global__ __launch_bounds__(kFp8MaxWaves * 64, 2) void fp8_stream_kernel(
     // each call: a load that may or may not have been issued would make every later
     // wait the longer one)
     auto pass = [&](Pass &b, Pass &next, uint32_t chunk, bool more) __attribute__((always_inline)) {
-        if (more) load(next, chunk + PASS);
+        if (more) load(next, chunk + kPass);
         compute(b, chunk);
     };
     Pass b0, b1;
     uint32_t chunk = first;
-    const uint32_t last = first + (end - first - 1) / PASS * PASS;
+    const uint32_t last = first + (end - first - 1) / kPass * kPass;
     load(b0, chunk);
     for (;;) {
         if (chunk == last) {
@@ -134,44 +121,30 @@ __global__ __launch_bounds__(kFp8MaxWaves * 64, 2) void fp8_stream_kernel(
             break;
         }
         pass(b0, b1, chunk, true);
-        chunk += PASS;
+        chunk += kPass;
         if (chunk == last) {
             pass(b1, b0, chunk, false);
             break;
         }
         pass(b1, b0, chunk, true);
-        chunk += PASS;
+        chunk += kPass;
     }
 
-    // the waves' sums, added in wave order, the tiles shared among the waves
+    // the waves' sums, added in wave order
     v4f *sums = reinterpret_cast<v4f *>(smem);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < CT; ++j) sums[((wave * MT + i) * CT + j) * 64 + lane] = acc[i][j];
+    for (int j = 0; j < CT; ++j) sums[(wave * CT + j) * 64 + lane] = acc[j];
     __syncthreads();
-    constexpr int kUnits = MT * (SILU ? CT / 2 : CT);
-    for (int u = wave; u < kUnits; u += nwaves) {
-        const int i = u / (kUnits / MT), j = u % (kUnits / MT);
-        v4f v = v4f{0, 0, 0, 0}, up = v;
-        for (int x = 0; x < nwaves; ++x) {
-            const v4f *of = sums + (x * MT + i) * CT * 64 + lane;
-            v += of[j * 64];
-            if constexpr (SILU) up += of[(j + CT / 2) * 64];
-        }
-        if constexpr (SILU)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = silu_product(v[r], up[r]);
-        const uint32_t row = 16 * i + c;
-        if (row < t.rows) store4(out, t.row0 + row, col0 + 16 * j + 4 * q, cols, v, wide);
+    if (wave != 0 || c >= t.rows) return;
+    v4f v = v4f{0, 0, 0, 0}, up = v;
+    for (int x = 0; x < nwaves; ++x) {
+        v += sums[x * CT * 64 + lane];
+        if constexpr (SILU) up += sums[(x * CT + 1) * 64 + lane];
     }
-}
-
-template <int MT, int CT, int PASS, bool SILU>
-void launch_stream(const Fp8Args &p, const Fp8StreamPlan &plan, bool wide, hipStream_t s) {
-    hipLaunchKernelGGL((fp8_stream_kernel<MT, CT, PASS, SILU>), dim3(plan.row_tiles * plan.col_tiles), dim3(64 * plan.waves),
-                       plan.lds, s, p.a, p.w, p.a_s, p.w_s, p.out, p.rows, p.n, p.k, plan.row_tiles, plan.col_tiles,
-                       plan.chunks_per_wave, wide);
+    if constexpr (SILU)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = silu_product(v[r], up[r]);
+    store4(out, t.row0 + c, col0 + 4 * q, cols, v, wide);
 }
 
 }  // namespace
@@ -179,8 +152,9 @@ void launch_stream(const Fp8Args &p, const Fp8StreamPlan &plan, bool wide, hipSt
 hipError_t launch_fp8_stream(const Fp8Args &p, const Fp8StreamPlan &plan, hipStream_t s) {
     const uint32_t cols = p.silu ? p.n / 2 : p.n;
     const bool wide = cols % 4 == 0 && reinterpret_cast<uintptr_t>(p.out) % 8 == 0;
-    if (p.silu) launch_stream<1, 2, 2, true>(p, plan, wide, s);
-    else launch_stream<1, 1, 2, false>(p, plan, wide, s);
+    auto kernel = p.silu ? fp8_stream_kernel<true> : fp8_stream_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3(plan.row_tiles * plan.col_tiles), dim3(64 * plan.waves), plan.lds, s, p.a, p.w, p.a_s,
+                       p.w_s, p.out, p.rows, p.n, p.k, plan.col_tiles, plan.chunks_per_wave, wide);
     return hipGetLastError();
 }
 
