@@ -365,7 +365,7 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
 }
 
 // The v-th tile: an expert's whole tiles down its rows, then along its columns, in
-// groups of up to six rows of tiles, so that what runs together shares A and W rows; then
+// groups of up to four rows of tiles, so that what runs together shares A and W rows; then
 // the experts' last rows along their columns.
 template <uint32_t BM>
 __device__ __forceinline__ RowTile place_tile(ClassedTiles<BM> &rt, uint32_t v, uint32_t tiles_n, uint32_t &tall,
@@ -383,7 +383,7 @@ __device__ __forceinline__ RowTile place_tile(ClassedTiles<BM> &rt, uint32_t v, 
             const uint32_t rows = __builtin_amdgcn_readlane(rt.full, o);
             const uint32_t olo = __builtin_amdgcn_readlane(rt.lo, o), ohi = __builtin_amdgcn_readlane(rt.hi, o);
             local -= (__builtin_amdgcn_readlane(rt.full_incl, o) - rows) * tiles_n;
-            const uint32_t groups = (rows + 5) / 6, size = (rows + groups - 1) / groups;
+            const uint32_t groups = (rows + 3) / 4, size = (rows + groups - 1) / groups;
             const uint32_t first = local / (size * tiles_n) * size, in = local % (size * tiles_n);
             tall = min(size, rows - first);
             place = in % tall;
