@@ -37,8 +37,8 @@ constexpr uint32_t kFp8PairIndex = kFp8NumShapes;
 BSR_HD constexpr Fp8Shape fp8_shape(uint32_t i) { return i == kFp8PairIndex ? kFp8Pair : kFp8Shapes[i]; }
 
 // ---- product, the weight streamed into registers ------------------------------
-// A workgroup owns 16 rows by 16 columns (and as many of the up half); its waves split K in chunks of 128, two of
-// them in flight.
+// A workgroup owns 16 rows by 16 columns (and as many of the up half); its waves split K
+// in chunks of 128, two of them in flight.
 constexpr uint32_t kFp8MaxWaves = 8;
 constexpr uint32_t kFp8Few = 4;  // rows (of an expert, on average) up to which it runs
 
@@ -96,9 +96,9 @@ inline uint64_t fp8_expected_tiles(uint32_t i, uint32_t rows, uint64_t used) {
 // Several experts with tiles for most of the CUs go by their rows on average, since
 // reading the weights is most of the time and wide tiles read them best: 64 x 128 below
 // 32 (64 experts of 8, n 4096, k 2048: 105 us, streamed 167, 32 x 128 126), 256 x 128
-// below 96 or while 256 x 256 has less than two rounds (6016 rows over 32 uneven experts, n
-// 2048, k 4096: 105, 256 x 256 119, 128 x 128 123, 64 x 128 122), else 256 x 256 (64 of 128,
-// n 4096, k 2048: 158, 256 x 128 171).
+// below 96 or while 256 x 256 has less than two rounds (6016 rows over 32 uneven experts,
+// n 2048, k 4096: 105, 256 x 256 119, 128 x 128 123, 64 x 128 122), else 256 x 256 (64 of
+// 128, n 4096, k 2048: 158, 256 x 128 171).
 // (128 x 64, whose two groups copy little each, is left to one weight: 3234 rows of 64
 // experts, n 256, k 7808: 55 us against 46 of 64 x 128.)
 inline Fp8Choice fp8_choice(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool silu) {

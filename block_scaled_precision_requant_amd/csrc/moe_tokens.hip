@@ -9,7 +9,10 @@
 //
 // All walk the tokens: a token's row is read once (dispatch, combine's gradient) or
 // written once, and each of its routed rows is read or written once, in runs of 16
-// bytes a lane.  Slots whose position is outside the rows are skipped.  Bound by HBM.
+// bytes a lane.  Slots whose position is outside the rows are skipped.  Bound by HBM
+// (a device copy of 1 GiB: 5.1 TB/s).  MI355X, 8192 tokens, top 8, n 4096: dispatch's
+// gradient 116 us, 5.2 TB/s; combine's 229, 5.0.  777 tokens, top 6, n 4095, rows at odd
+// alignments: dispatch 9.1 us, 4.9 TB/s.
 #include "fp8_internal.h"
 
 namespace bsr {

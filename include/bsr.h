@@ -468,7 +468,8 @@ BSR_API int w4a16_group_gemv_experts(const uint16_t *x, const uint8_t *w_packed,
  *             aligned; NULL if and only if w_qt is
  * Per block (the last block of rows may be shorter): s = fl32(amax / 448); s == 0
  * gives scale +0 and codes 0, else the E4M3 code nearest fl32(v / s), ties to the
- * even code, at most 448 in magnitude.
+ * even code, at most 448 in magnitude.  A NaN or Inf makes the scale of its own block
+ * NaN or Inf, and the block's codes unspecified.
  * Errors: BSR_EINVAL (k == 0, k % 128 != 0, n % 128 != 0 with w_qt, a launch of 2^32
  * threads: 256 per block), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.
  * experts == 0 or n == 0 is a valid empty problem.
@@ -534,8 +535,8 @@ BSR_API int fp8_grouped_gemm_blockscaled(const uint8_t *a_q, const uint8_t *w_q,
  *   out [rows, n]       BF16 as raw u16, 2-byte aligned
  * Limits: 1 <= top_k <= 16, n < 2^31.
  * Errors: BSR_EINVAL (those limits, a launch of 2^32 threads: 256 per 2048 columns of
- * a token, or per slot if those are more), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE, BSR_ELAUNCH.  tokens == 0,
- * n == 0 or rows == 0 is a valid empty problem.
+ * a token, or per slot if those are more), BSR_ENULL, BSR_EALIGN, BSR_EDEVICE,
+ * BSR_ELAUNCH.  tokens == 0, n == 0 or rows == 0 is a valid empty problem.
  */
 BSR_API int moe_dispatch(const uint16_t *x, const int32_t *pos, uint16_t *out, uint32_t tokens, uint32_t top_k,
                          uint32_t rows, uint32_t n, void *stream);

@@ -61,6 +61,20 @@ def test_values():
     check(w.bfloat16(), True)
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_not_finite_stays_in_its_block(value):
+    g = torch.Generator().manual_seed(3)
+    w = torch.randn(300, 384, generator=g).bfloat16()
+    want_q, want_s = fp8.quantize_w(w.float().numpy())
+    w[130, 200] = value  # block (1, 1)
+    q, s = torch.empty(300, 384, dtype=torch.uint8, device=DEV), torch.empty(3, 3, device=DEV)
+    bsr.quantize_w_fp8(w.to(DEV), q, s)
+    got_q, got_s = host(q), host(s)
+    assert not np.isfinite(got_s[1, 1])
+    got_s[1, 1], got_q[128:256, 128:256] = want_s[1, 1], want_q[128:256, 128:256]
+    assert np.array_equal(got_s, want_s) and np.array_equal(got_q, want_q)
+
+
 def test_two_dimensions_and_float8():
     w = torch.randn(256, 384, generator=torch.Generator().manual_seed(2)).bfloat16()
     q = torch.empty(256, 384, dtype=torch.float8_e4m3fn, device=DEV)
