@@ -11,7 +11,7 @@
 // written once, and each of its routed rows is read or written once, in runs of 16
 // bytes a lane.  Slots whose position is outside the rows are skipped.  Bound by HBM
 // (a device copy of 1 GiB: 5.1 TB/s).  MI355X, 8192 tokens, top 8, n 4096: dispatch's
-// gradient 116 us, 5.2 TB/s; combine's 229, 5.0.  777 tokens, top 6, n 4095, rows at odd
+// gradient 116 us, 5.2 TB/s; combine's 211, 5.4.  777 tokens, top 6, n 4095, rows at odd
 // alignments: dispatch 9.1 us, 4.9 TB/s.
 #include "fp8_internal.h"
 
@@ -60,7 +60,15 @@ __global__ __launch_bounds__(kTokenThreads) void combine_grad_kernel(
     const float *__restrict__ weights, uint16_t *d_y, float *__restrict__ d_weights, uint32_t top_k,
     uint32_t rows, uint32_t n) {
     __shared__ float sums[kTokenThreads / 64];
-    const uint32_t slot = blockIdx.x, t = slot / top_k;
+    // all slots of a token on one XCD, whose L2 reads the token's row once (8192 tokens,
+    // top 8, n 4096: 211 us; slots in the order of the grid, each on another XCD, 229)
+    const uint32_t wg = blockIdx.x, step = kXcds * top_k;
+    uint32_t slot = wg;
+    if (wg < gridDim.x / step * step) {
+        const uint32_t j = wg / kXcds;
+        slot = (j / top_k * kXcds + wg % kXcds) * top_k + j % top_k;
+    }
+    const uint32_t t = slot / top_k;
     const uint32_t p = (uint32_t)pos[slot];
     if (p >= rows) {
         if (threadIdx.x == 0) d_weights[slot] = 0.0f;
