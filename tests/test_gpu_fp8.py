@@ -256,6 +256,34 @@ def test_data_gradient_on_the_transposed_weight(shape):
             assert res.ok, str(res)
 
 
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("scale", [0.25, 2.0 ** -6, 2.0 ** -20, 2.0 ** 30])
+def test_silu_over_its_range(rows, scale):
+    """Gates of every code of both signs times `scale` (up to 112, and far past it), exact in binary32, ups of the row's
+    own scale; streamed rows and tiles."""
+    n, k = 512, 128
+    w = np.zeros((1, n, k), np.uint8)
+    w[0, :128, 0] = np.minimum(np.arange(128), 126)      # gates, two blocks of them
+    w[0, 128:256, 0] = w[0, :128, 0] | 0x80
+    w[0, 256:, 0] = 0x38                                 # ups: 1
+    w_s = np.array([scale, scale, 1, 1], np.float32).reshape(1, 4, 1)
+    a = np.zeros((rows, k), np.uint8)
+    a[:, 0] = 0x38
+    a_s = (2.0 ** -(np.arange(rows) % 5)).astype(np.float32)[:, None]
+    got = run_grouped(a, w, a_s, w_s, np.array([0, rows]), None, rows, True)
+    got = torch.from_numpy(got.view(np.int16)).view(torch.bfloat16).double().numpy()
+    g = a_s.astype(np.float64) * np.concatenate((fp8.E4M3[w[0, :128, 0]], fp8.E4M3[w[0, 128:256, 0]])) * scale
+    y = g / (1 + np.exp(-np.clip(g, -700, 700))) * a_s
+    # the kernel's own steps, one rounding to BF16 (half of eps 2^-7) and half its smallest step; below -88.7 exp(-gate) is past binary32
+    # and the result 0, which leaves out less than 89 * 2^-128
+    tol = np.abs(y) * ((1.25 * np.abs(g) + 8) * 2.0 ** -24 + 2.0 ** -8 * (1 + 2.0 ** -9)) + 2.0 ** -134
+    tol[g < -88.7] = 89 * 2.0 ** -128
+    assert np.isfinite(got).all()
+    bad = np.argwhere(~(np.abs(got - y) <= tol))
+    assert not len(bad), [(g[i, j], got[i, j], y[i, j]) for i, j in bad[:4]]
+    assert np.array_equal(np.signbit(got)[g != 0], np.signbit(g)[g != 0])  # (a sum of zeros of both signs is +0)
+
+
 def test_dense_equals_one_expert():
     rng = np.random.default_rng(11)
     for m, n, k in ((7, 256, 384), (600, 512, 256)):
