@@ -39,6 +39,10 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 
 // BF16 nearest to x, ties to even, and NaN for NaN (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint16_t f32_to_bf16(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+__device__ __forceinline__ uint2 f32_to_bf16x4(v4f v) {
+    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint2, __builtin_convertvector(v, b4));
+}
 
 // Sixteen rows of E4M3 codes times sixteen others over one block of 128: lane l holds
 // 32 codes of row l % 16 of `w` and of `a`, the same elements of the block for both;
@@ -86,8 +90,7 @@ __device__ __forceinline__ void store4(uint16_t *out, uint64_t row, uint32_t col
     uint16_t *p = out + row * n + col;
     if (wide) {
         if (col < n)
-            *reinterpret_cast<ushort4 *>(p) =
-                make_ushort4(f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3]));
+            *reinterpret_cast<uint2 *>(p) = f32_to_bf16x4(v);
         return;
     }
 #pragma unroll

@@ -359,8 +359,7 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = silu_product(v[r], acc[i][j + TN / 2][r]);
             const uint32_t row = i / KG * 16 + c, chunk = (2 * j + q / 2) ^ (row % kChunks);
-            *reinterpret_cast<ushort4 *>(mine + row * kRow + chunk * 16 + q % 2 * 8) =
-                make_ushort4(f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3]));
+            *reinterpret_cast<uint2 *>(mine + row * kRow + chunk * 16 + q % 2 * 8) = f32_to_bf16x4(v);
         }
     }
 #pragma unroll
