@@ -286,11 +286,14 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
                 const int j = column(i, u), jb = column((i + TM - 1) % TM, u);
                 // the next copies of stage b + RING - 1, one by one between the matrix products: several
                 // behind one another would hold up the wave; a ring of 2 needs them in the first half, and all
-                // go out before the barrier, whose wait counts whole stages
-                constexpr int kSlots = TM == 1 ? 0 : (RING == 2 ? TM * TN / 2 : (TM - 1) * TN);
+                // go out before the barrier, whose wait counts whole stages (with one row of tiles they
+                // went out above)
+                if constexpr (TM > 1) {
+                    constexpr int kSlots = RING == 2 ? TM * TN / 2 : (TM - 1) * TN;
 #pragma unroll
-                for (int x = 0; x < kCopies; ++x)
-                    if (x * kSlots / kCopies == i * TN + u) copy(x, b + RING - 1, free_slot);
+                    for (int x = 0; x < kCopies; ++x)
+                        if (x * kSlots / kCopies == i * TN + u) copy(x, b + RING - 1, free_slot);
+                }
                 p[i & 1][j] = fp8_dot16(wf[j], af[i % kAf]);
                 if (i + 1 == TM) wf[j] = operand(w0, w1, j);
                 if (i + 1 == TM && u + 1 == TN) af[0] = operand(a0, a1, 0);
