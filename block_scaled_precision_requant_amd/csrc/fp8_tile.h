@@ -365,6 +365,8 @@ __device__ __forceinline__ void fp8_tile(char *smem, const Fp8Tile &t, uint16_t 
             *reinterpret_cast<uint2 *>(mine + row * kRow + chunk * 16 + q % 2 * 8) = f32_to_bf16x4(v);
         }
     }
+    // (other lanes' values are read: a wave's LDS accesses run in order, and the compiler keeps it)
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (uint32_t r0 = 0; r0 < kOwn; r0 += 64 / kChunks) {
         const uint32_t own = r0 + lane / kChunks, chunk = lane % kChunks;
