@@ -52,8 +52,8 @@ int quantize_w_fp8(const uint16_t *w_bf16, uint8_t *w_q, float *w_scale, uint8_t
     if (!w_bf16 || !w_q || !w_scale || (w_qt == nullptr) != (w_scale_t == nullptr)) return BSR_ENULL;
     if (!aligned(w_bf16, 16) || !aligned(w_q, 16) || !aligned(w_scale, 4) || !aligned(w_qt, 16) || !aligned(w_scale_t, 4))
         return BSR_EALIGN;
-    const uint64_t blocks = div_up(n, kFp8Block) * (k / kFp8Block);  // (below 2^50)
-    if (blocks > kMaxThreads || experts * blocks * bsr::kQwThreads > kMaxThreads) return BSR_EINVAL;
+    const uint64_t blocks = div_up(n, kFp8Block) * (k / kFp8Block);  // (below 2^50: of all experts it may pass 64 bits)
+    if (blocks > kMaxThreads / bsr::kQwThreads / experts) return BSR_EINVAL;
     if (int st = check_device()) return st;
     return launched(bsr::launch_quantize_w_fp8(w_bf16, w_q, w_scale, w_qt, w_scale_t, experts, n, k,
                                                static_cast<hipStream_t>(stream)));

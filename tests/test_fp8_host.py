@@ -45,6 +45,15 @@ def test_quantize_refusals(change, status):
     assert _call("quantize_w_fp8", QUANT, **change) == status
 
 
+# sizes whose number of threads passes 64 bits: 2^56 blocks, as many and a few, just under 2^64
+@pytest.mark.parametrize("change", [
+    dict(experts=1 << 31, n=1 << 20, k=1 << 19), dict(experts=1 << 31, n=(1 << 20) + 1, k=1 << 19),
+    dict(experts=(1 << 32) - 1, n=(1 << 32) - 128, k=128), dict(experts=(1 << 32) - 1, n=1, k=128 * ((1 << 25) - 1)),
+    dict(experts=1 << 31, n=1 << 20, k=1 << 19, qt=FAKE, st=FAKE)])
+def test_quantize_refuses_thread_counts_past_64_bits(change):
+    assert _call("quantize_w_fp8", QUANT, **change) == INV
+
+
 BOTH = [(dict(k=0), INV), (dict(k=64), INV), (dict(k=1 << 23), INV), (dict(n=1 << 31), INV), (dict(n=0), OK),
         (dict(a=None), NUL), (dict(w=None), NUL), (dict(a_s=None), NUL), (dict(w_s=None), NUL), (dict(out=None), NUL),
         (dict(a=_fake(8)), ALI), (dict(w=_fake(8)), ALI), (dict(a_s=_fake(2)), ALI), (dict(w_s=_fake(2)), ALI),
