@@ -56,11 +56,13 @@ __device__ __forceinline__ v4f fp8_dot16(v8i w, v8i a) {
 // hardware's 2^t and the quotient by its reciprocal, each good to one step of binary32; t is
 // rounded, which for a negative gate moves the result by up to 1.25 |gate| 2^-24, below
 // 2^-17 where it is not 0 (BF16 rounds at 2^-8).  The reciprocal is of a quarter, so that it
-// is normal for every finite exp(-gate).  (8192 rows over 8 uneven experts, n 28672, k 4096:
+// is normal for every finite exp(-gate); its own quarter is 2^-22 off at most where that is
+// subnormal (gate below -87.3, where the bound has 2^-18 to spare), while a quarter of the gate
+// would cut a subnormal gate's bits.  (8192 rows over 8 uneven experts, n 28672, k 4096:
 // 934 us; with expf and a division 982, the epilogue being a tenth of a tile's time.)
 __device__ __forceinline__ float silu_product(float gate, float up) {
     const float e = __builtin_amdgcn_exp2f(gate * -1.44269504f);
-    return gate * 0.25f * __builtin_amdgcn_rcpf(fmaf(e, 0.25f, 0.25f)) * up;
+    return gate * (__builtin_amdgcn_rcpf(fmaf(e, 0.25f, 0.25f)) * 0.25f) * up;
 }
 
 // Eight elements of a row of n, from c on; rows of any alignment (one 16-byte access at

@@ -512,7 +512,8 @@ BSR_API int fp8_gemm_blockscaled(const uint8_t *a_q, const uint8_t *w_q, const f
  *   silu_mul 0: out [rows, n].  1: columns 0..n/2-1 of the weight are the gate and
  *           n/2..n-1 the up projection, out [rows, n/2] = bf16_rne( fl32(gate /
  *           fl32(1 + exp(-gate))) * up ), gate and up in binary32, the value before it is
- *           rounded to BF16 within (1.25 |gate| + 8) 2^-24 of it; n % 256 == 0
+ *           rounded to BF16 within (1.25 |gate| + 8) 2^-24 of it, or where the quotient is
+ *           subnormal within a step of it, 2^-149 |up|; n % 256 == 0
  * Limits: experts <= 65536, rows and n < 2^31, k < 2^23, and with row_index a_rows *
  * k < 2^32 (the rows are gathered with 32-bit offsets).
  * Errors: as fp8_gemm_blockscaled; BSR_EINVAL too for a_rows too small (NULL

@@ -284,6 +284,30 @@ def test_silu_over_its_range(rows, scale):
     assert np.array_equal(np.signbit(got)[g != 0], np.signbit(g)[g != 0])  # (a sum of zeros of both signs is +0)
 
 
+@pytest.mark.parametrize("rows", [3, 40])
+def test_silu_of_subnormal_gates(rows):
+    """Gates of every code times 2^-140, whole steps of binary32's smallest, and ups large enough that the product is an
+    ordinary BF16: the quotient is the nearest step."""
+    n, k = 512, 128
+    w = np.zeros((1, n, k), np.uint8)
+    w[0, :128, 0] = np.minimum(np.arange(128), 126)
+    w[0, 128:256, 0] = w[0, :128, 0] | 0x80
+    w[0, 256:, 0] = 0x38                                 # 1
+    w_s = np.array([2.0 ** -70, 2.0 ** -70, 2.0 ** 127, 2.0 ** 127], np.float32).reshape(1, 4, 1)
+    a = np.zeros((rows, k), np.uint8)
+    a[:, 0] = 0x38
+    a_s = np.full((rows, 1), 2.0 ** -70, np.float32)
+    got = run_grouped(a, w, a_s, w_s, np.array([0, rows]), None, rows, True)
+    got = torch.from_numpy(got.view(np.int16)).view(torch.bfloat16).double().numpy()
+    g, up = np.concatenate((fp8.E4M3[w[0, :128, 0]], fp8.E4M3[w[0, 128:256, 0]])) * 2.0 ** -140, 2.0 ** 57
+    y = g / (1 + np.exp(-g)) * up
+    # the quotient's rounding is half a step of 2^-149 there (past it by less than the 2^-20 of what it rounds); then the
+    # kernel's own steps and one rounding to BF16, as in test_silu_over_its_range
+    tol = up * 2.0 ** -150 * (1 + 2.0 ** -20) + np.abs(y) * (8 * 2.0 ** -24 + 2.0 ** -8 * (1 + 2.0 ** -9))
+    bad = np.argwhere(~(np.abs(got - y) <= tol))
+    assert not len(bad), [(g[j] * 2.0 ** 149, got[i, j] / up * 2.0 ** 149) for i, j in bad[:4]]
+
+
 def test_dense_equals_one_expert():
     rng = np.random.default_rng(11)
     for m, n, k in ((7, 256, 384), (600, 512, 256)):
