@@ -642,10 +642,23 @@ def moe_prefill_fp8(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale
     """One expert layer on FP8 weights (quantize_w_fp8), for any number of tokens: as moe_prefill, with w_gate_up
     [E,2I,H] and w_down [E,H,I] in E4M3 codes and their scales (H and I multiples of 128), in six steps: router,
     activation quantizer, grouped gate and up with the SiLU product, its quantizer, grouped down, weighted sum."""
-    t, (hidden, inter) = _layer_tokens(x_bf16, logits, out, residual), w_down.shape[1:]
+    t, (experts, hidden, inter) = _layer_tokens(x_bf16, logits, out, residual), w_down.shape
     if hidden % 128 or inter % 128:
         raise ValueError(f"w_down: shape {tuple(w_down.shape)}, its last two sizes must be multiples of 128")
-    s = scratch
+    s, dev = scratch, x_bf16.get_device()
+    # (what a later step refuses is refused before the first)
+    if max(hidden, inter) >> 23 or t * hidden >> 32:
+        raise ValueError(f"{t} tokens, w_down {tuple(w_down.shape)}: widths must be below 2^23, the activations below 2^32 codes")
+    _arg(x_bf16, (t, hidden), BF16, "x_bf16", dev)
+    if logits.shape != (t, experts):
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected {(t, experts)}")
+    _e4m3(w_gate_up, (experts, 2 * inter, hidden), "w_gate_up", dev)
+    _arg(gate_up_scale, (experts, 2 * inter // 128, hidden // 128), F32, "gate_up_scale", dev)
+    _e4m3(w_down, (experts, hidden, inter), "w_down", dev)
+    _arg(down_scale, (experts, hidden // 128, inter // 128), F32, "down_scale", dev)
+    held = s.a_i8.shape[1], s.h.shape[1], s.offsets.shape[0] - 1
+    if held != (hidden, inter, experts):
+        raise ValueError(f"scratch: hidden, inter, experts {held}, the weights have {(hidden, inter, experts)}")
     rows = s.route(logits, score=score, renorm=renorm, scale=scale, stream=stream)
 
     def codes(q, q_scale, n, width):  # of n rows, in the scratch of the int8 layer: bytes, and fewer scales
@@ -653,7 +666,7 @@ def moe_prefill_fp8(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale
 
     a_q, a_scale = codes(s.a_i8, s.a_scale, t, hidden)
     h_q, h_scale = codes(s.h_i8, s.h_scale, rows, inter)
-    h, y, dev = s.h[:rows], s.y[:rows], x_bf16.get_device()
+    h, y = s.h[:rows], s.y[:rows]
     with _on(dev):  # (the quantizers run on the current device)
         quantize_act(x_bf16, a_q, a_scale, group=128, fmt=FMT_E4M3, stream=stream)
     fp8_grouped_gemm_blockscaled(a_q, w_gate_up, a_scale, gate_up_scale, s.offsets, h, row_index=s.row_token[:rows],

@@ -255,6 +255,56 @@ def test_layer_refusals(launched):
         assert not launched, change
 
 
+@pytest.mark.parametrize("arg", ["x_bf16", "logits", "w_gate_up", "gate_up_scale", "w_down", "down_scale", "out", "residual"])
+def test_layer_checks_each_argument_before_any_launch(arg, launched):
+    """Another element type, another size in each dimension, strides, another device."""
+    layer = Layer()
+    t = layer.args.get(arg, layer.args["out"])
+    wrong = {F32: torch.float64, BF: torch.float16, U8: I8, E4: torch.float8_e5m2}[t.dtype]
+    bad = [t.view(wrong) if t.element_size() == wrong.itemsize else t.to(wrong), t.as_subclass(Card1),
+           t.transpose(-1, -2).contiguous().transpose(-1, -2)]
+    assert not bad[-1].is_contiguous() or 1 in t.shape[-2:]
+    bad += [zeros(*(n + 128 * (i == j) for i, n in enumerate(t.shape)), dt=t.dtype) for j in range(t.dim())]
+    for i, b in enumerate(bad):
+        if i == 2 and b.is_contiguous():
+            continue
+        with pytest.raises(ValueError):
+            layer(**{arg: b})
+        assert not launched, (i, launched)
+
+
+@pytest.mark.parametrize("other", [dict(h=256), dict(i=128), dict(experts=5)])
+def test_layer_refuses_scratch_of_other_sizes(other, launched):
+    layer = Layer()
+    layer.scratch = Layer(**other).scratch
+    with pytest.raises(ValueError, match="scratch"):
+        layer()
+    assert not launched
+
+
+@pytest.mark.parametrize("sizes", [dict(h=1 << 23, i=128), dict(h=128, i=1 << 23)])
+def test_layer_refuses_widths_past_the_products(sizes, launched):
+    """A product ends below 2^23 elements a row; no memory stands behind these tensors."""
+    meta = lambda *s, dt=BF: torch.empty(s, dtype=dt, device="meta")  # noqa: E731
+    t, e, h, i = 2, 2, sizes["h"], sizes["i"]
+    scratch = bsr.MoeScratch(t, e, 1, h, i, device="meta")
+    with pytest.raises(ValueError, match=r"2\^23"):
+        bsr.moe_prefill_fp8(meta(t, h), meta(t, e, dt=F32), meta(e, 2 * i, h, dt=E4), meta(e, 2 * i // 128, h // 128, dt=F32),
+                            meta(e, h, i, dt=E4), meta(e, h // 128, i // 128, dt=F32), meta(t, h), scratch)
+    assert not launched
+
+
+def test_layer_refuses_tokens_past_the_gather(launched):
+    """Gathered rows end at 2^32 bytes."""
+    meta = lambda *s, dt=BF: torch.empty(s, dtype=dt, device="meta")  # noqa: E731
+    t, e, h, i = 1 << 19, 2, 8192, 128
+    scratch = bsr.MoeScratch(t, e, 1, h, i, device="meta")
+    with pytest.raises(ValueError, match=r"2\^32"):
+        bsr.moe_prefill_fp8(meta(t, h), meta(t, e, dt=F32), meta(e, 2 * i, h, dt=E4), meta(e, 2 * i // 128, h // 128, dt=F32),
+                            meta(e, h, i, dt=E4), meta(e, h // 128, i // 128, dt=F32), meta(t, h), scratch)
+    assert not launched
+
+
 def test_layer_runs_on_its_tensors_device(monkeypatch):
     """Every step runs with its tensors' device as the current one, whichever is current around the call."""
     current, seen = [0], []
