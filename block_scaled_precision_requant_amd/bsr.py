@@ -624,6 +624,8 @@ def fp8_grouped_gemm_blockscaled(a_q, w_q, a_scale, w_scale, offsets, out, row_i
 def prefill_fp8(a_bf16, w_q, w_scale, a_q_scratch, a_scale_scratch, out, stream=None):
     """The projection on an FP8 weight, in two launches: quantize_act (E4M3, group 128), then fp8_gemm_blockscaled."""
     m, k = a_bf16.shape
+    if k >> 23:
+        raise ValueError(f"a_bf16: shape {(m, k)}, rows must be below 2^23 elements")
     dev = a_bf16.get_device()
     _arg(a_bf16, (m, k), BF16, "a_bf16", dev)  # (all of the second launch's arguments are looked at before the first)
     _e4m3(a_q_scratch, (m, k), "a_q_scratch", dev)

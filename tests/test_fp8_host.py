@@ -305,6 +305,16 @@ def test_layer_refuses_tokens_past_the_gather(launched):
     assert not launched
 
 
+def test_prefill_refuses_a_width_past_the_product(launched):
+    """Before the quantizer runs."""
+    meta = lambda *s, dt=BF: torch.empty(s, dtype=dt, device="meta")  # noqa: E731
+    k = 1 << 23
+    with pytest.raises(ValueError, match=r"2\^23"):
+        bsr.prefill_fp8(meta(2, k), meta(4, k, dt=E4), meta(1, k // 128, dt=F32), meta(2, k, dt=E4), meta(2, k // 128, dt=F32),
+                        meta(2, 4))
+    assert not launched
+
+
 def test_layer_runs_on_its_tensors_device(monkeypatch):
     """Every step runs with its tensors' device as the current one, whichever is current around the call."""
     current, seen = [0], []
