@@ -18,14 +18,21 @@ inline bool fp8_k_ok(uint32_t k) { return k != 0 && k % kFp8Block == 0 && k < kF
 // ---- product, tiles through LDS ---------------------------------------------
 // Shapes of a workgroup's tile, in the order of kFp8Shapes.  `cost`: tenths of a
 // microsecond that one round of workgroups on every CU takes at k = 4096 (MI355X, the
-// weight in the cache behind the L2); `last`: the same where a last round leaves half of
-// the places empty.
+// weight in the cache behind the L2, one call behind the other from the host, of which none
+// takes less than 6.5); `last`: the same where a last round leaves half of the places
+// empty.  They serve to order the shapes.  In captured graphs the rounds take 51 (half empty
+// 39), 47, 61, 122; 49, 52, 72, 161; 62, 71, 105, 162; 140, 218, 367, 590, the pair 367 (301).
+// Over 330 sizes of 5 to 8192 rows, the weight in the cache and past it, the shape taken is
+// 1.3 % behind the best of the 17 on average, 24 % at most (64 rows, n 4096, k 14336: 64 x 16
+// 18.7 us, 32 x 32 15.1).  64 x 128 is counted once a CU although two fit: counted twice
+// (242, half empty 162) the average is 2.6 %, and 300 x 8192 x 8192 (past
+// the cache) would take it at 53 us instead of 128 x 128 at 36.
 struct Fp8Shape {
     uint16_t bm, bn, threads, per_cu, cost, last;
 };
 constexpr uint32_t kFp8NumShapes = 16;
 constexpr Fp8Shape kFp8Shapes[kFp8NumShapes] = {
-    {16, 16, 256, 2, 71, 65},     {16, 32, 256, 1, 70, 70},    {16, 64, 256, 1, 87, 87},    {16, 128, 256, 1, 142, 142},
+    {16, 16, 256, 2, 66, 65},     {16, 32, 256, 1, 66, 66},    {16, 64, 256, 1, 87, 87},    {16, 128, 256, 1, 142, 142},
     {32, 16, 256, 1, 66, 66},     {32, 32, 256, 1, 72, 72},    {32, 64, 256, 1, 102, 102},  {32, 128, 192, 1, 158, 158},
     {64, 16, 256, 1, 71, 71},     {64, 32, 256, 1, 84, 84},    {64, 64, 256, 1, 116, 116},  {64, 128, 256, 1, 170, 170},
     {128, 64, 512, 1, 160, 160},  {128, 128, 512, 1, 243, 243}, {256, 128, 512, 1, 404, 404}, {256, 256, 512, 1, 530, 530},
@@ -85,20 +92,28 @@ inline uint64_t fp8_expected_tiles(uint32_t i, uint32_t rows, uint64_t used) {
     return tiles > used ? tiles : used;
 }
 
-// The weight alone is read for up to kFp8Few rows (1 / 4 / 8 rows, n 28672, k 4096:
-// streamed 23.6 / 24.4 / 28.1 us, in tiles 27.8 / 28.1 / 28.1).  Else the shape whose
-// rounds cost least: one round on all CUs if any shape has one, so that for few rows the
-// columns, for many the tile's area, are what grows.  Measured against its neighbours
-// (us; rows, n, k; the chosen shape first): 64, 4096, 14336: 64 x 16 18.0, 64 x 32 20.4;
-// 256, 4096, 4096: 64 x 64 11.6, 128 x 64 13.9, 64 x 32 14.9; 512, 4096, 14336: 128 x 64
-// 43.6, 64 x 128 51, 128 x 128 58; 128, 28672, 8192: 128 x 128 62, 64 x 128 72; 1024,
-// 14336, 4096: 256 x 256 63, pairs 77; 2048, 4096, 14336: 256 x 128 129, pairs 143.
+// Up to kFp8Few rows (of an expert) the weight alone is read, streamed.  Both sides (us;
+// weights past the cache; 1 / 4 / 5 rows, streamed and the best tiles): n 28672, k 4096 24.0 /
+// 23.9 / 24.5, 16 x 128 24.6 throughout; n 4096, k 14336 13.7 / 13.1 / 13.3, 16 x 16 13.6 / 13.1 /
+// 13.0; n 28672, k 256 5.0 / 5.3 / 5.3, 5.4; n 28672, k 8192 50 / 48 / -, 16 x 16 44 / 43 / -; 64
+// experts of 1 / 4 / 5 / 8 rows, n 4096, k 2048 93 / 92 / 93 / 98, 64 x 128 90 / 91 / 91 / 92; 32,
+// n 2048, k 4096 55 / 54 / 55 / 63, 63 throughout.
+// Else the shape whose rounds cost least: one round on all CUs if any shape has one, so that
+// for few rows the columns, for many the tile's area, are what grows.  Measured against its
+// neighbours (us; rows, n, k; the chosen shape first; the weight in the cache): 16, 4096,
+// 14336: 16 x 16 12.0, 16 x 32 12.2, 32 x 32 13.8; 256, 4096, 4096: 64 x 64 11.1, 128 x 64
+// 12.6, 64 x 32 13.6; 512, 4096, 14336: 128 x 64 40.5, 64 x 128 48, 128 x 128 56; 128, 28672,
+// 8192: 128 x 128 39.5, 64 x 128 42.8; 1024, 14336, 4096: 256 x 256 54, pairs 63; 2048, 4096,
+// 14336, past the cache: 256 x 128 120, pairs 136.
 // Several experts with tiles for most of the CUs go by their rows on average, since
 // reading the weights is most of the time and wide tiles read them best: 64 x 128 below
-// 32 (64 experts of 8, n 4096, k 2048: 105 us, streamed 167, 32 x 128 126), 256 x 128
-// below 96 or while 256 x 256 has less than two rounds (6016 rows over 32 uneven experts,
-// n 2048, k 4096: 105, 256 x 256 119, 128 x 128 123, 64 x 128 122), else 256 x 256 (64 of
-// 128, n 4096, k 2048: 158, 256 x 128 171).
+// 32, 256 x 128 below 96 or while 256 x 256 has less than two rounds, else 256 x 256.  Both
+// sides, even and (uneven) counts: 64 experts of 8, n 4096, k 2048: 64 x 128 92 (91), 256 x 128
+// 104 (104), 32 x 128 118 (118).  Of 32: 64 x 128 96 (103), 256 x 128 110 (111); 16 of 32, n
+// 8192, k 4096: 121 (129), 134 (120).  Of 64: 122 (146), 136 (118), so the border stands where
+// uneven counts turn.  64 of 96, n 4096, k 2048: 256 x 128 130 (136), 256 x 256 134 (136); of
+// 160: 171 (175), 163 (169); of 512: 353 (392), 286 (336); of 16 of 96, n 8192, k 4096, 138 (143),
+// 144 (176).
 // (128 x 64, whose two groups copy little each, is left to one weight: 3234 rows of 64
 // experts, n 256, k 7808: 55 us against 46 of 64 x 128.)
 inline Fp8Choice fp8_choice(uint32_t rows, uint32_t experts, uint32_t n, uint32_t k, bool silu) {
