@@ -654,10 +654,9 @@ def moe_prefill_fp8(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale
     _arg(x_bf16, (t, hidden), BF16, "x_bf16", dev)
     if logits.shape != (t, experts):
         raise ValueError(f"logits: shape {tuple(logits.shape)}, expected {(t, experts)}")
-    _e4m3(w_gate_up, (experts, 2 * inter, hidden), "w_gate_up", dev)
-    _arg(gate_up_scale, (experts, 2 * inter // 128, hidden // 128), F32, "gate_up_scale", dev)
-    _e4m3(w_down, (experts, hidden, inter), "w_down", dev)
-    _arg(down_scale, (experts, hidden // 128, inter // 128), F32, "down_scale", dev)
+    w13, w2 = _e4m3(w_gate_up, (experts, 2 * inter, hidden), "w_gate_up", dev), _e4m3(w_down, (experts, hidden, inter), "w_down", dev)
+    s13 = _arg(gate_up_scale, (experts, 2 * inter // 128, hidden // 128), F32, "gate_up_scale", dev)
+    s2 = _arg(down_scale, (experts, hidden // 128, inter // 128), F32, "down_scale", dev)
     held = s.a_i8.shape[1], s.h.shape[1], s.offsets.shape[0] - 1
     if held != (hidden, inter, experts):
         raise ValueError(f"scratch: hidden, inter, experts {held}, the weights have {(hidden, inter, experts)}")
@@ -671,11 +670,14 @@ def moe_prefill_fp8(x_bf16, logits, w_gate_up, gate_up_scale, w_down, down_scale
     h, y = s.h[:rows], s.y[:rows]
     with _on(dev):  # (the quantizers run on the current device)
         quantize_act(x_bf16, a_q, a_scale, group=128, fmt=FMT_E4M3, stream=stream)
-    fp8_grouped_gemm_blockscaled(a_q, w_gate_up, a_scale, gate_up_scale, s.offsets, h, row_index=s.row_token[:rows],
-                                 silu_mul=True, stream=stream)
+    # (looked at above: the products are launched as fp8_grouped_gemm_blockscaled does)
+    off = s.offsets.data_ptr()
+    _launch("fp8_grouped_gemm_blockscaled", dev, stream, a_q.data_ptr(), w13, a_scale.data_ptr(), s13, off,
+            s.row_token.data_ptr(), 1, h.data_ptr(), t, rows, experts, 2 * inter, hidden)
     with _on(dev):
         quantize_act(h, h_q, h_scale, group=128, fmt=FMT_E4M3, stream=stream)
-    fp8_grouped_gemm_blockscaled(h_q, w_down, h_scale, down_scale, s.offsets, y, stream=stream)
+    _launch("fp8_grouped_gemm_blockscaled", dev, stream, h_q.data_ptr(), w2, h_scale.data_ptr(), s2, off, None, 0,
+            y.data_ptr(), rows, rows, experts, hidden, inter)
     moe_combine(y, s.pos[:t], s.weights[:t], out, residual=residual, stream=stream)
 
 
