@@ -9,7 +9,7 @@
 // leave as whole 128-byte lines too.  Bound by HBM: 3 bytes an element, 4 with the
 // transposed codes.  MI355X, 8 weights of 4096 x 4096 with the transposed codes (537
 // MB): 105 us, 5.1 TB/s, as a device copy of 1 GiB reaches; vector issue, for the
-// divisions and conversions, is at 68 % beside it.  One of 1000 x 2048 takes 6.2.
+// divisions and conversions, is at 65 % beside it.  One of 1000 x 2048 takes 6.2.
 #include "fp8_internal.h"
 
 namespace bsr {

@@ -15,10 +15,10 @@
 //
 // In this layout a load touches 16 rows and moves 16 bytes a clock and CU, 9.7 TB/s over
 // the chip: enough for the weight alone, which is why rows past kFp8Few run in the tiles
-// of fp8_tile.h.  MI355X: one row, n 28672, k 4096 / 8192 (117 / 235 MB) 23.6 / 46.7 us,
+// of fp8_tile.h.  MI355X: one row, n 28672, k 4096 / 8192 (117 / 235 MB) 23.2 / 45.5 us,
 // 5.0 TB/s, as a device copy of 1 GiB reaches; n 4096, k 14336 (59 MB, which the 256 MB
 // cache holds between calls) 11.2 us; 256 rows through the gate and up projections of 64
-// uneven experts, n 4096, k 2048, 83 us.
+// uneven experts, n 4096, k 2048, 82 us.
 #include "fp8_internal.h"
 
 namespace bsr {

@@ -24,7 +24,7 @@
 //    costs 9 cycles: the loop is written as product, one copy, four FMAs.
 //  * The stage's barrier stands before its last 16 rows, so that the next stage's first
 //    operands are read while those are computed.
-//  * 8192 x 28672 x 8192: 1.54-1.58 ms by the card, 2.4-2.5 PFLOP/s, the matrix cores busy for 65 % of it.
+//  * 8192 x 28672 x 8192: 1.52-1.58 ms by the card, 2.4-2.5 PFLOP/s, the matrix cores busy for 65 % of it.
 //    Zeros instead of data took 1.32 ms where data took 1.6: the clock falls with the
 //    energy of the products (a library product of that size without block scales:
 //    1.19-1.34 ms by its data).
@@ -428,8 +428,8 @@ __device__ __forceinline__ uint32_t grouped_run(uint32_t wg, uint32_t total) {
 // are counted from the offsets, so that every XCD gets its share of them, in falling
 // order of work; an expert's last rows, when a half or a quarter of the tile holds them,
 // take waves of as many rows less (8192 rows over 8 uneven experts, n 28672, k 4096, with
-// the SiLU product: 934 us, 2.06 PFLOP/s; the last rows' waves and the order took it from
-// 1157 to 1060).
+// the SiLU product: 935-980 us by the card, 2.0 PFLOP/s; the last rows' waves and the order
+// took 8 % off it).
 template <int BM, int BN, int WM, int WN, int RING, int KG, bool SILU, Rows ROWS>
 __global__ __launch_bounds__((Fp8Geo<BM, BN, WM, WN, RING, KG>::kThreads),
                              (Fp8Geo<BM, BN, WM, WN, RING, KG>::kPerSimd)) void fp8_gemm_kernel(

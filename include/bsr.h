@@ -561,7 +561,8 @@ BSR_API int moe_dispatch_grad(const uint16_t *d_rows, const int32_t *pos, uint16
  * A slot whose p is outside [0, rows) has d_weights 0 and touches no row; rows of d_y
  * that no slot names are left as they were.  Where several slots name one row
  * (moe_route's pos has no such pair) each element of it is one of theirs, not the
- * sum, and with d_y = y their d_weights are unspecified.  The order of a sum follows n; equal calls give equal bits.
+ * sum, and with d_y = y their d_weights are unspecified.  The order of a sum follows
+ * n; equal calls give equal bits.
  *   d_out   [tokens, n]     BF16 as raw u16, 2-byte aligned
  *   y, d_y  [rows, n]       BF16 as raw u16, 2-byte aligned; d_y may be y
  *   pos     [tokens, top_k] i32, weights, d_weights [tokens, top_k] f32, 4-byte aligned
