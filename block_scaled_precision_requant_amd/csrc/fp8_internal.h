@@ -57,7 +57,7 @@ __device__ __forceinline__ v4f fp8_dot16(v8i w, v8i a) {
 // rounded, which for a negative gate moves the result by up to 1.25 |gate| 2^-24, below
 // 2^-17 where it is not 0 (BF16 rounds at 2^-8).  The reciprocal is of a quarter, so that it
 // is normal for every finite exp(-gate); its own quarter is 2^-22 off at most where that is
-// subnormal (gate below -87.3, where the bound has 2^-18 to spare), while a quarter of the gate
+// subnormal (gate below -87.3, where the bound has 2^-19 to spare), while a quarter of the gate
 // would cut a subnormal gate's bits.  (8192 rows over 8 uneven experts, n 28672, k 4096, in
 // one comparison: 934 us, with expf and a division 982, the epilogue being a tenth of a tile's time.)
 __device__ __forceinline__ float silu_product(float gate, float up) {
